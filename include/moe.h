@@ -403,6 +403,92 @@ int moe_forward(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const f
                 const moe_weights_t *w, moe_bf16_t *out, const moe_aux_t *aux, void *ws,
                 size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------
+ * Decoding with these layers: the layer for a few tokens, the linear maps
+ * around it, and the check of a drafted block (SpecForge PR #943: a drafter
+ * of MoE layers drafts 7-token blocks that the target verifies).
+ * --------------------------------------------------------------------- */
+
+/* The whole layer for at most MOE_FEW_MAX_TOKENS tokens in one kernel launch:
+ * arguments and meaning as moe_forward, for decode steps and single drafted
+ * blocks, where the launches of moe_forward and the waits between them cost
+ * as much as the weights.  Routing, top-p and budget follow the same rules
+ * (equal logits: lower id; sums in slot order); logits made by the projection
+ * and the softmax's sum are added in another order than moe_router_logits and
+ * moe_route add them, so weights can differ by ulps from theirs.  The
+ * intermediate activations keep 16 significant bits (a bf16 and its bf16
+ * remainder) and the experts' outputs are summed in fp32 and rounded once, so
+ * `out` is closer to the fp32 result than moe_forward's, and not the same bits.
+ * The result is the same bits on every run.
+ *   - T > MOE_FEW_MAX_TOKENS returns MOE_ERR_UNSUPPORTED.
+ *   - aux->counts, offsets, perm and slot_pos must be NULL (nothing is
+ *     dispatched).  aux->logits receives projected logits, as in moe_forward.
+ *   - Uses the workspace of moe_workspace_bytes(cfg, T), zeroed once
+ *     (moe_status_clear); a launch leaves its counters at zero.  One workspace
+ *     serves one stream at a time.
+ *   - The kernel is a cooperative launch of one block per SM (its blocks wait
+ *     for one another, each wait bounded: MOE_STATUS_TIMEOUT); it can be
+ *     captured into a CUDA graph.  Where such a launch is impossible it
+ *     returns MOE_ERR_CUDA.
+ *   - out must not overlap an input. */
+#define MOE_FEW_MAX_TOKENS 16
+int moe_forward_few(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const float *logits,
+                    const moe_weights_t *w, moe_bf16_t *out, const moe_aux_t *aux, void *ws, size_t ws_bytes,
+                    void *stream);
+/* The same with MXFP8 or NVFP4 expert weights (H, I and Is multiples of 128). */
+int moe_forward_few_mxfp8(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const float *logits,
+                          const moe_weights_mxfp8_t *w, moe_bf16_t *out, const moe_aux_t *aux, void *ws,
+                          size_t ws_bytes, void *stream);
+int moe_forward_few_nvfp4(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const float *logits,
+                          const moe_weights_nvfp4_t *w, moe_bf16_t *out, const moe_aux_t *aux, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/* Linear map with its epilogue: out = residual + act(x W^T + bias), bf16
+ * operands, fp32 sums and epilogue, rounded once to bf16 (out_f32 = 0) or not
+ * at all (out_f32 = 1: e.g. a head's logits).
+ *   x [T, K]; w [N, K]; bias [N] or NULL; residual [T, N] or NULL; out [T, N]
+ *   bf16 or f32.  activation: MOE_ACT_* (GELU is the erf form).
+ *   - T >= 0 (0: no-op), N >= 1, K >= 8 a multiple of 8, T * N and N * K below
+ *     2^40; any other size is as good (no multiple of a tile is asked for).
+ *   - out may be `residual` itself (bf16), in place; it must not overlap
+ *     anything else.
+ *   - ws: moe_linear_workspace_bytes(T, N, K) bytes (0 for bad sizes), zeroed
+ *     once by moe_status_clear; one workspace serves one stream at a time. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_GELU 2
+#define MOE_ACT_SILU 3
+size_t moe_linear_workspace_bytes(int32_t T, int32_t N, int32_t K);
+int moe_linear(int32_t T, int32_t N, int32_t K, const moe_bf16_t *x, const moe_bf16_t *w, const moe_bf16_t *bias,
+               int32_t activation, const moe_bf16_t *residual, void *out, int32_t out_f32, void *ws,
+               size_t ws_bytes, void *stream);
+
+/* Verification of drafted tokens (speculative sampling with given random
+ * numbers).  For each of B requests, with x_i = draft_tokens[i], p_i and q_i
+ * the target's and the drafter's probabilities at position i:
+ *   token i stays while u_i q_i(x_i) < p_i(x_i) (accept_u; compared in fp64);
+ *   at the first refused token j the next token is drawn from
+ *   max(p_j - q_j, 0), after a whole block (length l) from p_l; drawing takes
+ *   the first v whose running sum over 0..v passes sample_u times the total
+ *   (fp64 sums in token order; rounding past the end: the last v with mass).
+ *   tokens[b] = the kept tokens, the drawn one, then -1; n_accepted[b] = how
+ *   many stayed.
+ * target_probs [B, L + 1, V] f32; draft_probs [B, L, V] f32, or NULL: the
+ * drafter put all its mass on the drafted token (q = 1 there); draft_tokens
+ * [B, L]; draft_len [B], or NULL: every block has L tokens (clamped to
+ * [0, L]; nothing behind a block's length is looked at); accept_u [B, L],
+ * sample_u [B] f32 in [0, 1); tokens [B, L + 1], n_accepted [B] i32.
+ *   - A drafted token outside [0, V) ends its block there.
+ *   - Rows need not sum to 1.  NaN, infinite and negative entries of p - q
+ *     carry no mass; a drafted token whose comparison sees a NaN is refused.
+ *   - A refused token whose row has p <= q everywhere (rounded inputs) is
+ *     drawn from p; a row without any mass gives -1.
+ *   - sample_u below 0 or NaN counts as 0.
+ *   - B = 0 is a no-op; L >= 0; V >= 1; B < 2^27.  No workspace. */
+int moe_verify(int32_t B, int32_t L, int32_t V, const float *target_probs, const float *draft_probs,
+               const int32_t *draft_tokens, const int32_t *draft_len, const float *accept_u, const float *sample_u,
+               int32_t *tokens, int32_t *n_accepted, void *stream);
+
 /* Status word: MOE_STATUS_* bits set by kernels (sticky until cleared).
  * moe_status_read enqueues a copy on `stream`, waits for the stream, and
  * returns MOE_OK with *status_out filled (host pointer).  moe_status_clear

@@ -29,6 +29,8 @@ __all__ = [
     "MoEWeightsMXFP8", "moe_mxfp8_pack_scales", "moe_expert_ffn_mxfp8", "moe_forward_mxfp8", "pack_mxfp8",
     "MoEWeightsNVFP4", "moe_nvfp4_pack_scales", "moe_expert_ffn_nvfp4", "moe_forward_nvfp4", "pack_nvfp4",
     "moe_ep_rank_ids", "moe_ep_pack", "moe_ep_unpack",
+    "moe_forward_few", "moe_forward_few_mxfp8", "moe_forward_few_nvfp4", "FEW_MAX_TOKENS",
+    "moe_linear", "linear_workspace_bytes", "moe_verify",
     "status_read", "status_clear",
     "EXPORTED_SYMBOLS", "MOE_STATUS_TIMEOUT",
 ]
@@ -44,8 +46,12 @@ EXPORTED_SYMBOLS = (
     "moe_mxfp8_pack_scales", "moe_expert_ffn_mxfp8", "moe_forward_mxfp8",
     "moe_nvfp4_pack_scales", "moe_expert_ffn_nvfp4", "moe_forward_nvfp4",
     "moe_ep_rank_ids", "moe_ep_pack", "moe_ep_unpack",
+    "moe_forward_few", "moe_forward_few_mxfp8", "moe_forward_few_nvfp4",
+    "moe_linear_workspace_bytes", "moe_linear", "moe_verify",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20  # MOE_NOALLOC_SCRATCH_BYTES
+FEW_MAX_TOKENS = 16  # MOE_FEW_MAX_TOKENS
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}  # MOE_ACT_*
 MOE_STATUS_TIMEOUT = 1
 MOE_STATUS_BOUNDS = 2
 MOE_STATUS_NONFINITE = 4
@@ -236,10 +242,17 @@ def load_library(build_if_stale: bool = True, variant: str = "release"):
         lib.moe_expert_ffn_nvfp4.argtypes = [cfg, i32, P, P, P, P, P, P, ctypes.POINTER(_WeightsNVFP4), P, P, sz, P]
         lib.moe_forward_nvfp4.argtypes = [cfg, i32, P, P, ctypes.POINTER(_WeightsNVFP4), P, ctypes.POINTER(_Aux), P,
                                           sz, P]
+        for name, wt in (("moe_forward_few", _Weights), ("moe_forward_few_mxfp8", _WeightsMXFP8),
+                         ("moe_forward_few_nvfp4", _WeightsNVFP4)):
+            getattr(lib, name).argtypes = [cfg, i32, P, P, ctypes.POINTER(wt), P, ctypes.POINTER(_Aux), P, sz, P]
+        lib.moe_linear_workspace_bytes.restype = sz
+        lib.moe_linear_workspace_bytes.argtypes = [i32, i32, i32]
+        lib.moe_linear.argtypes = [i32, i32, i32, P, P, P, i32, P, P, i32, P, sz, P]
+        lib.moe_verify.argtypes = [i32, i32, i32, P, P, P, P, P, P, P, P, P]
         lib.moe_error_string.restype = ctypes.c_char_p
         lib.moe_error_string.argtypes = [ctypes.c_int]
         for name in EXPORTED_SYMBOLS:
-            if name not in ("moe_workspace_bytes", "moe_error_string"):
+            if name not in ("moe_workspace_bytes", "moe_linear_workspace_bytes", "moe_error_string"):
                 getattr(lib, name).restype = ctypes.c_int
         if variant == "release":
             _lib = lib
@@ -554,6 +567,124 @@ def moe_forward(cfg: MoEConfig, x, logits, weights: MoEWeights, out, ws, *, aux:
     _check("moe_forward", load_library().moe_forward(
         ctypes.byref(cfg._c()), T, _ptr(x), _ptr(logits, True), ctypes.byref(w), _ptr(out), ctypes.byref(a),
         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def _expect_like(t, dtype, shape, device, name: str):
+    """Host-side check of one tensor of a call: type, shape and device."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+
+
+def _current_device(t, name: str):
+    """The launch goes to the current device: its tensors have to live there."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _forward_few(fn: str, cfg: MoEConfig, x, logits, weights, out, ws, aux, stream):
+    import torch
+    dev = _current_device(x, "x")
+    T, H, E, I, Is = x.shape[0], cfg.hidden, cfg.n_routed_experts, cfg.moe_intermediate_size, \
+        cfg.shared_intermediate_size
+    _expect_like(x, torch.bfloat16, (T, H), dev, "x")
+    _expect_like(out, torch.bfloat16, (T, H), dev, "out")
+    if logits is not None:
+        _expect_like(logits, torch.float32, (T, E), dev, "logits")
+    elif weights.w_router is None:
+        raise ValueError("logits is None and the weights have no w_router")
+    else:
+        _expect_like(weights.w_router, torch.bfloat16, (E, H), dev, "w_router")
+    if weights.w_gate.shape[:2] != (E, I) or weights.w_down.shape[:2] != (E, H):
+        raise ValueError("the expert weights' shapes differ from the configuration's")
+    if Is and (weights.ws_gate is None or weights.ws_gate.shape[0] != Is):
+        raise ValueError("the shared expert's weights differ from the configuration's")
+    w, a = weights._c(), _Aux()
+    for name, t in (aux or {}).items():
+        setattr(a, name, _ptr(t))
+    _check(fn, getattr(load_library(), fn)(
+        ctypes.byref(cfg._c()), T, _ptr(x), _ptr(logits, True), ctypes.byref(w), _ptr(out), ctypes.byref(a),
+        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_forward_few(cfg: MoEConfig, x, logits, weights: MoEWeights, out, ws, *, aux: Optional[dict] = None,
+                    stream=None):
+    """The whole layer for at most FEW_MAX_TOKENS tokens in one kernel
+    (arguments as moe_forward; aux without counts, offsets, perm, slot_pos)."""
+    _forward_few("moe_forward_few", cfg, x, logits, weights, out, ws, aux, stream)
+
+
+def moe_forward_few_mxfp8(cfg: MoEConfig, x, logits, weights: MoEWeightsMXFP8, out, ws, *,
+                          aux: Optional[dict] = None, stream=None):
+    """moe_forward_few with MXFP8 expert weights."""
+    _forward_few("moe_forward_few_mxfp8", cfg, x, logits, weights, out, ws, aux, stream)
+
+
+def moe_forward_few_nvfp4(cfg: MoEConfig, x, logits, weights: MoEWeightsNVFP4, out, ws, *,
+                          aux: Optional[dict] = None, stream=None):
+    """moe_forward_few with NVFP4 expert weights."""
+    _forward_few("moe_forward_few_nvfp4", cfg, x, logits, weights, out, ws, aux, stream)
+
+
+def linear_workspace_bytes(T: int, N: int, K: int) -> int:
+    """Workspace of moe_linear for x [T, K] and w [N, K] (status_clear it once)."""
+    n = load_library().moe_linear_workspace_bytes(T, N, K)
+    if n == 0:
+        raise MoEError("moe_linear_workspace_bytes", -1, "invalid sizes")
+    return int(n)
+
+
+def moe_linear(x, w, out, ws, *, bias=None, activation: str = "none", residual=None, stream=None):
+    """out [T, N] = residual + act(x [T, K] . w [N, K]^T + bias): bf16 in, out
+    bf16 or fp32 by its type; activation "none", "relu", "gelu" (erf) or
+    "silu"; out may be `residual` itself."""
+    import torch
+    dev = _current_device(x, "x")
+    (T, K), N = x.shape, w.shape[0]
+    _expect_like(x, torch.bfloat16, (T, K), dev, "x")
+    _expect_like(w, torch.bfloat16, (N, K), dev, "w")
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out: expected bfloat16 or float32, got {out.dtype}")
+    _expect_like(out, out.dtype, (T, N), dev, "out")
+    if bias is not None:
+        _expect_like(bias, torch.bfloat16, (N,), dev, "bias")
+    if residual is not None:
+        _expect_like(residual, torch.bfloat16, (T, N), dev, "residual")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation: one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    _check("moe_linear", load_library().moe_linear(
+        T, N, K, _ptr(x), _ptr(w), _ptr(bias, True), ACTIVATIONS[activation], _ptr(residual, True), _ptr(out),
+        int(out.dtype == torch.float32), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_verify(target_probs, draft_tokens, accept_u, sample_u, tokens, n_accepted, *, draft_probs=None,
+               draft_len=None, stream=None):
+    """Drafted tokens [B, L] against the target's probabilities [B, L + 1, V]
+    with given random numbers accept_u [B, L] and sample_u [B]: tokens
+    [B, L + 1] receives the kept tokens, the drawn one and -1 behind it,
+    n_accepted [B] how many stayed.  draft_probs [B, L, V], or None for a
+    drafter that puts all its mass on its token; draft_len [B] for blocks
+    shorter than L."""
+    import torch
+    dev = _current_device(target_probs, "target_probs")
+    B, L1, V = target_probs.shape
+    L = L1 - 1
+    f32, i32 = torch.float32, torch.int32
+    _expect_like(target_probs, f32, (B, L1, V), dev, "target_probs")
+    _expect_like(draft_tokens, i32, (B, L), dev, "draft_tokens")
+    _expect_like(accept_u, f32, (B, L), dev, "accept_u")
+    _expect_like(sample_u, f32, (B,), dev, "sample_u")
+    _expect_like(tokens, i32, (B, L1), dev, "tokens")
+    _expect_like(n_accepted, i32, (B,), dev, "n_accepted")
+    if draft_probs is not None:
+        _expect_like(draft_probs, f32, (B, L, V), dev, "draft_probs")
+    if draft_len is not None:
+        _expect_like(draft_len, i32, (B,), dev, "draft_len")
+    _check("moe_verify", load_library().moe_verify(
+        B, L, V, _ptr(target_probs), _ptr(draft_probs, True), _ptr(draft_tokens), _ptr(draft_len, True),
+        _ptr(accept_u), _ptr(sample_u), _ptr(tokens), _ptr(n_accepted), _stream(stream)))
 
 
 def status_read(ws, stream=None) -> int:

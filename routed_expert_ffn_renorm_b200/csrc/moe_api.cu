@@ -5,6 +5,8 @@
 #include <cstring>
 #include <mutex>
 
+#include "few.cuh"
+#include "linear.cuh"
 #include "moe_internal.cuh"
 
 using namespace moe;
@@ -13,14 +15,18 @@ namespace {
 
 constexpr size_t kAlign = 256;
 // Head of the workspace: [0, 256) status word and work-item counters,
-// [256, 256 + 4 * (E + 2)) gate/up completion counters of the fused FFN.
+// [256, 256 + 4 * (E + 2)) gate/up completion counters of the fused FFN,
+// [4608, 8192) counters of the few-token layer and the linear map.
 constexpr size_t kHeadBytes = 8192;
 constexpr size_t kHdoneOffset = 256;
+constexpr size_t kSyncOffset = 4608;
+static_assert(kHdoneOffset + 4 * (kMaxExperts + 2) <= kSyncOffset, "workspace head");
+static_assert(kSyncOffset + 4 * kFewSyncInts <= kHeadBytes, "workspace head");
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct WsLayout {
     size_t status, idx, w, sgate, keff, kept, ndrop, counts, offsets, perm, slot_pos, hist, bagg, bcnt;
-    size_t x_perm, h_perm, h_shared, ybuf, logits, rpart, total;
+    size_t x_perm, h_perm, h_shared, ybuf, logits, rpart, few, total;
 };
 
 WsLayout ws_layout(const moe_config_t &c, int T) {
@@ -53,6 +59,10 @@ WsLayout ws_layout(const moe_config_t &c, int T) {
     L.ybuf = take((size_t)T * (c.num_experts_per_tok + 1) * c.hidden * 2);
     L.logits = take((size_t)T * E * 4);
     L.rpart = take(rp_partial_bytes(T, (int)E, c.hidden));
+    L.few = T <= kFewMaxTokens
+                ? take(few_h_bytes(T, (int)E, c.moe_intermediate_size, c.num_experts_per_tok,
+                                   c.shared_intermediate_size))
+                : off;
     L.total = off;
     return L;
 }
@@ -629,6 +639,166 @@ int moe_forward_nvfp4(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, c
                             return moe_expert_ffn_nvfp4(cfg, T, x, x_perm, offsets, perm, tw, sgate, w, ybuf, ws,
                                                         ws_bytes, stream);
                         });
+}
+
+}  // extern "C"
+
+namespace {
+
+// The few-token layer around its weights: `m` holds the matrices in the order
+// gate, up, down, shared gate, shared up, shared down.
+int few_impl(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const float *logits, const FewMatrix (&m)[6],
+             int fmt, const moe_bf16_t *w_router, const moe_bf16_t *ws_gate_vec, moe_bf16_t *out,
+             const moe_aux_t *aux, void *ws, size_t ws_bytes, void *stream) {
+    const bool sh = cfg->shared_intermediate_size > 0;
+    if (T > kFewMaxTokens) return MOE_ERR_UNSUPPORTED;
+    if (fmt != 0 && (cfg->hidden % 128 != 0 || cfg->moe_intermediate_size % 128 != 0 ||
+                     cfg->shared_intermediate_size % 128 != 0))
+        return MOE_ERR_UNSUPPORTED;
+    if (!aligned(x) || !aligned_or_null(logits) || !aligned(out) || !aligned(ws)) return MOE_ERR_INVALID_ARG;
+    if ((!logits && !aligned(w_router)) || (sh && !aligned(ws_gate_vec))) return MOE_ERR_INVALID_ARG;
+    for (int i = 0; i < (sh ? 6 : 3); ++i)
+        if (!aligned(m[i].w) || (fmt != 0 && !aligned(m[i].sf)) || (fmt == 2 && !f32_aligned(m[i].ts)))
+            return MOE_ERR_INVALID_ARG;
+    moe_aux_t a{};
+    if (aux) a = *aux;
+    if (a.counts || a.offsets || a.perm || a.slot_pos) return MOE_ERR_INVALID_ARG;  // nothing is dispatched
+    if (!aligned_or_null(a.topk_idx) || !aligned_or_null(a.topk_w) || !aligned_or_null(a.sgate) ||
+        !aligned_or_null(a.keff) || !aligned_or_null(a.logits))
+        return MOE_ERR_INVALID_ARG;
+    const WsLayout L = ws_layout(*cfg, T);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    FewArgs f{};
+    f.T = T;
+    f.H = cfg->hidden;
+    f.E = cfg->n_routed_experts;
+    f.I = cfg->moe_intermediate_size;
+    f.k = cfg->num_experts_per_tok;
+    f.Is = cfg->shared_intermediate_size;
+    f.norm_topk = cfg->norm_topk;
+    f.budget = cfg->budget;
+    f.topp = cfg->topp;
+    f.x = x;
+    f.w_router = w_router;
+    f.gvec = ws_gate_vec;
+    f.project = logits == nullptr;
+    f.logits = logits ? const_cast<float *>(logits) : a.logits ? a.logits : at<float>(ws, L.logits);
+    f.gate = m[0];
+    f.up = m[1];
+    f.down = m[2];
+    f.s_gate = m[3];
+    f.s_up = m[4];
+    f.s_down = m[5];
+    f.idx = a.topk_idx;
+    f.w = a.topk_w;
+    f.sgate = sh ? (a.sgate ? a.sgate : at<float>(ws, L.sgate)) : nullptr;
+    f.keff = a.keff;
+    f.kept = a.expert_kept;
+    f.n_dropped = a.n_dropped;
+    f.out = out;
+    f.h = at<uint8_t>(ws, L.few);
+    f.status = at<int32_t>(ws, L.status);
+    f.sync = at<int32_t>(ws, kSyncOffset);
+    if constexpr (kDebugBounds)  // checked library: non-finite given logits are reported, not routed silently
+        if (logits) {
+            const int rc = cuda_rc(launch_check_logits((long long)T * f.E, logits, f.status, as_stream(stream)));
+            if (rc) return rc;
+        }
+    return cuda_rc(launch_few(f, fmt, as_stream(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_forward_few(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const float *logits,
+                    const moe_weights_t *w, moe_bf16_t *out, const moe_aux_t *aux, void *ws, size_t ws_bytes,
+                    void *stream) {
+    const int rc = check_config(cfg, T);
+    if (rc || T == 0) return rc;
+    if (!w) return MOE_ERR_INVALID_ARG;
+    const FewMatrix m[6] = {{w->w_gate, nullptr, nullptr},  {w->w_up, nullptr, nullptr},
+                            {w->w_down, nullptr, nullptr},  {w->ws_gate, nullptr, nullptr},
+                            {w->ws_up, nullptr, nullptr},   {w->ws_down, nullptr, nullptr}};
+    return few_impl(cfg, T, x, logits, m, 0, w->w_router, w->ws_gate_vec, out, aux, ws, ws_bytes, stream);
+}
+
+int moe_forward_few_mxfp8(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const float *logits,
+                          const moe_weights_mxfp8_t *w, moe_bf16_t *out, const moe_aux_t *aux, void *ws,
+                          size_t ws_bytes, void *stream) {
+    const int rc = check_config(cfg, T);
+    if (rc || T == 0) return rc;
+    if (!w) return MOE_ERR_INVALID_ARG;
+    const FewMatrix m[6] = {{w->w_gate, w->w_gate_scale, nullptr},   {w->w_up, w->w_up_scale, nullptr},
+                            {w->w_down, w->w_down_scale, nullptr},   {w->ws_gate, w->ws_gate_scale, nullptr},
+                            {w->ws_up, w->ws_up_scale, nullptr},     {w->ws_down, w->ws_down_scale, nullptr}};
+    return few_impl(cfg, T, x, logits, m, 1, w->w_router, w->ws_gate_vec, out, aux, ws, ws_bytes, stream);
+}
+
+int moe_forward_few_nvfp4(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const float *logits,
+                          const moe_weights_nvfp4_t *w, moe_bf16_t *out, const moe_aux_t *aux, void *ws,
+                          size_t ws_bytes, void *stream) {
+    const int rc = check_config(cfg, T);
+    if (rc || T == 0) return rc;
+    if (!w) return MOE_ERR_INVALID_ARG;
+    const float *ts = w->ws_tscale;
+    const FewMatrix m[6] = {{w->w_gate, w->w_gate_scale, w->w_gate_tscale},
+                            {w->w_up, w->w_up_scale, w->w_up_tscale},
+                            {w->w_down, w->w_down_scale, w->w_down_tscale},
+                            {w->ws_gate, w->ws_gate_scale, ts},
+                            {w->ws_up, w->ws_up_scale, ts ? ts + 1 : nullptr},
+                            {w->ws_down, w->ws_down_scale, ts ? ts + 2 : nullptr}};
+    return few_impl(cfg, T, x, logits, m, 2, w->w_router, w->ws_gate_vec, out, aux, ws, ws_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_linear(int32_t T, int32_t N, int32_t K) {
+    if (T < 0 || N < 1 || K < 8) return MOE_ERR_INVALID_ARG;
+    if (K % 8 != 0 || (long long)T * N >= (1ll << 40) || (long long)N * K >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_linear_workspace_bytes(int32_t T, int32_t N, int32_t K) {
+    if (check_linear(T, N, K) != MOE_OK) return 0;
+    return kHeadBytes + align_up(linear_scratch_bytes(T, N, K));
+}
+
+int moe_linear(int32_t T, int32_t N, int32_t K, const moe_bf16_t *x, const moe_bf16_t *w, const moe_bf16_t *bias,
+               int32_t activation, const moe_bf16_t *residual, void *out, int32_t out_f32, void *ws,
+               size_t ws_bytes, void *stream) {
+    const int rc = check_linear(T, N, K);
+    if (rc) return rc;
+    if (activation < MOE_ACT_NONE || activation > MOE_ACT_SILU || (out_f32 != 0 && out_f32 != 1))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!aligned(x) || !aligned(w) || !aligned_or_null(bias) || !aligned_or_null(residual) || !aligned(out) ||
+        !aligned(ws) || (out_f32 && static_cast<const void *>(residual) == out))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < moe_linear_workspace_bytes(T, N, K)) return MOE_ERR_WORKSPACE;
+    const LinearArgs a{T,   N,       K, x, w, bias, residual, activation, out, out_f32, at<int32_t>(ws, 0),
+                       at<int32_t>(ws, kSyncOffset), at<float>(ws, kHeadBytes)};
+    return cuda_rc(launch_linear(a, as_stream(stream)));
+}
+
+int moe_verify(int32_t B, int32_t L, int32_t V, const float *target_probs, const float *draft_probs,
+               const int32_t *draft_tokens, const int32_t *draft_len, const float *accept_u, const float *sample_u,
+               int32_t *tokens, int32_t *n_accepted, void *stream) {
+    if (B < 0 || L < 0 || L > (1 << 20) || V < 1) return MOE_ERR_INVALID_ARG;
+    if (B >= (1 << 27)) return MOE_ERR_UNSUPPORTED;
+    if (B == 0) return MOE_OK;
+    if (!aligned(target_probs) || !aligned_or_null(draft_probs) || !aligned_or_null(draft_len) ||
+        !aligned(sample_u) || !aligned(tokens) || !aligned(n_accepted) ||
+        (L > 0 && (!aligned(draft_tokens) || !aligned(accept_u))))
+        return MOE_ERR_INVALID_ARG;
+    return cuda_rc(launch_verify(B, L, V, target_probs, draft_probs, draft_tokens, draft_len, accept_u, sample_u,
+                                 tokens, n_accepted, as_stream(stream)));
 }
 
 int moe_status_read(const void *ws, int32_t *status_out, void *stream) {

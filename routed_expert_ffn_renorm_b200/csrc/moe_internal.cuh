@@ -133,6 +133,11 @@ cudaError_t launch_ep_unpack(int n_max, const int32_t *n_dev, int k, int H, cons
 cudaError_t launch_combine(int T, int k, int H, int has_shared, const uint16_t *ybuf,
                            const int32_t *keff, uint16_t *out, cudaStream_t st);
 
+// Verification of drafted tokens (verify.cu); arguments as moe_verify.
+cudaError_t launch_verify(int B, int L, int V, const float *p, const float *q, const int32_t *draft,
+                          const int32_t *len, const float *u, const float *us, int32_t *tokens, int32_t *n_accepted,
+                          cudaStream_t st);
+
 // Grouped expert FFN (tcgen05).
 struct FfnArgs {
     int T, H, E, I, k, Is;
