@@ -306,7 +306,7 @@ def _layer_handle(s, moe):
     names = {"w_gate": "gate", "w_up": "up", "w_down": "down"}
     if c["Is"]:
         names.update(ws_gate="s_gate", ws_up="s_up", ws_down="s_down")
-    kw = {n: s[m]["w"] for n, m in names.items()}
+    kw = {n: s[m]["w"][0] if n.startswith("ws_") else s[m]["w"] for n, m in names.items()}
     if fmt != "bf16":
         kw.update({n + "_scale": s[m]["s"] for n, m in names.items()})
     if fmt == "nvfp4":
