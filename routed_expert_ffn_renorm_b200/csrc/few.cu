@@ -8,9 +8,32 @@
 // the gate weight folded into h, so that the down projection is one product
 // over the concatenated intermediate channels of the experts in use.
 //
-// One cooperative grid, one CTA per SM.  Every CTA routes all tokens itself
-// (the routing is a few microseconds of work and saves a launch and a round
-// trip); the grid meets twice: after the projection's logits, and after h.
+// Bound: every weight of the experts in use crosses HBM once; with at most 16
+// tokens the arithmetic is a few percent of that time.  So the kernel is one
+// weight stream.  A cooperative grid, one CTA per SM, walks three lists of
+// 128-row weight chunks -- the shared expert's gate/up (64 channels: 64 gate
+// and 64 up rows), the routed experts' gate/up, the down projection -- each
+// list cut into equal contiguous shares, so that all SMs stream until the end
+// whatever the sizes.  A share's ends fall inside row blocks: those blocks'
+// sums go to the workspace as fp32 partials, and the last CTA to arrive adds
+// them in CTA order (the same bits on every run).
+//
+// Roles: one producer warp streams weight chunks into a shared-memory ring by
+// TMA, running ahead over everything the weights do not depend on -- the
+// shared expert's while the tokens are still being routed, the down
+// projection's while h is still being made; a second one loads the matching
+// token operand (x, or h after the grid barrier) for the same ring slots; 16
+// consumer warps do the rest.  The consumers multiply with mma.sync: its 16 x
+// 8 x 16 tile takes 16 weight rows by 8 tokens, so that 1..8 tokens waste no
+// operand traffic, and the weights go from shared memory straight to
+// registers; tcgen05 would pad the tokens and stage converted weights through
+// tensor memory for no gain, the tensor pipe being idle most of the time
+// either way.  The grid barrier between h and the down projection is hidden
+// behind the ring, which holds 4 us of the stream.
+//
+// h is kept as a bf16 and its bf16 remainder (two token operands, one weight
+// operand): 16 significant bits, so that the result differs from fp32
+// arithmetic by its final rounding only.
 #include <atomic>
 
 #include "few.cuh"
@@ -23,9 +46,12 @@ namespace moe {
 namespace {
 using namespace tc;
 
-constexpr int kFewThreads = 512;
-constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewGroups = 2;                    // consumer groups: each takes its share of a chunk's K steps
+constexpr int kFewConsumers = kFewGroups * 256;  // 8 warps of 16 weight rows per group
+constexpr int kFewThreads = kFewConsumers + 64;  // + weight producer, token producer
 constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;
+constexpr int kFewMaxSms = 160;
+constexpr int kFewSmem = 227 * 1024;
 
 struct FewRouting {
     int32_t idx[kFewMaxSlots];
@@ -34,36 +60,36 @@ struct FewRouting {
     uint32_t mask[kMaxExperts];  // tokens of each expert
     float agg[kMaxExperts];
     uint16_t list[kFewMaxSlots];  // experts in use, ascending
-    int nu, ndrop, stop;
+    int nu, ndrop;
 };
 
-// Every CTA of the grid has arrived on *ctr (from zero) and its writes are visible.
-__device__ bool grid_meet(int32_t *ctr, int32_t *status, int *stop) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        atomicAdd(ctr, 1);
-        const unsigned long long t0 = globaltimer();
-        *stop = 0;
-        while (ld_acquire(ctr) < (int)gridDim.x)
-            if (globaltimer() - t0 > kWaitLimitNs) {
-                atomicOr(status, MOE_STATUS_TIMEOUT);
-                *stop = 1;
-                break;
-            }
-    }
-    __syncthreads();
-    return *stop == 0;
+// Arrive on a grid barrier (one thread, after a barrier of the writers), and wait for all of the grid.
+__device__ __forceinline__ void grid_arrive(int32_t *ctr) {
+    __threadfence();
+    atomicAdd(ctr, 1);
 }
+__device__ __forceinline__ bool grid_wait(int32_t *ctr, volatile int *abort_flag, int32_t *status) {
+    const unsigned long long t0 = globaltimer();
+    while (ld_acquire(ctr) < (int)gridDim.x) {
+        if (*abort_flag) return false;
+        if (globaltimer() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            atomicOr(status, MOE_STATUS_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void consumers_sync() { named_bar_sync(1, kFewConsumers); }
 
 template <int V>
 __device__ __noinline__ int few_route_token(int t, const FewArgs &a, FewRouting &r, int lane) {
     return route_token<V, false>(t, a.E, a.k, a.norm_topk, a.topp, a.logits, r.idx, r.w, nullptr, lane);
 }
 
-// Route all tokens, apply the budget, list the experts in use (whole block).
+// Route all tokens, apply the budget, list the experts in use (all consumer warps).
 __device__ void few_route(const FewArgs &a, FewRouting &r) {
-    const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, Tk = a.T * a.k;
+    const int tid = threadIdx.x, nthr = kFewConsumers, lane = tid & 31, Tk = a.T * a.k;
     for (int t = tid >> 5; t < a.T; t += nthr >> 5) {
         int c;
         if (a.E <= 128)
@@ -77,16 +103,16 @@ __device__ void few_route(const FewArgs &a, FewRouting &r) {
         if (lane == 0) r.keff[t] = c;
     }
     for (int e = tid; e < kMaxExperts; e += nthr) r.mask[e] = 0;
-    __syncthreads();
+    consumers_sync();
     for (int s = tid; s < Tk; s += nthr)
         if (r.idx[s] >= 0 && r.idx[s] < a.E) atomicOr(&r.mask[r.idx[s]], 1u << (s / a.k));
-    __syncthreads();
+    consumers_sync();
     int mine = 0;
     for (int e = tid; e < a.E; e += nthr) mine += r.mask[e] != 0;
     if (tid == 0) r.nu = 0;
-    __syncthreads();
+    consumers_sync();
     if (mine) atomicAdd(&r.nu, mine);
-    __syncthreads();
+    consumers_sync();
     const int nu = r.nu;
     const bool cut = a.budget > 0 && nu > a.budget;
     if (cut) {
@@ -98,9 +124,9 @@ __device__ void few_route(const FewArgs &a, FewRouting &r) {
                     if (r.idx[i] == e) s += r.w[i];
             r.agg[e] = s;
         }
-        __syncthreads();
+        consumers_sync();
         // rank in (sum descending, id ascending); the others leave
-        bool drop[(kMaxExperts + 255) / 256];
+        bool drop[kMaxExperts / kFewConsumers];
         int n = 0;
         for (int e = tid; e < a.E; e += nthr, ++n) {
             int rank = 0;
@@ -108,11 +134,11 @@ __device__ void few_route(const FewArgs &a, FewRouting &r) {
                 rank += r.mask[o] != 0 && (r.agg[o] > r.agg[e] || (r.agg[o] == r.agg[e] && o < e));
             drop[n] = r.mask[e] == 0 || rank >= a.budget;
         }
-        __syncthreads();
+        consumers_sync();
         n = 0;
         for (int e = tid; e < a.E; e += nthr, ++n)
             if (drop[n]) r.mask[e] = 0;
-        __syncthreads();
+        consumers_sync();
         for (int t = tid; t < a.T; t += nthr) {
             int32_t *ti = r.idx + t * a.k;
             float *tw = r.w + t * a.k;
@@ -138,7 +164,7 @@ __device__ void few_route(const FewArgs &a, FewRouting &r) {
             r.keff[t] = c;
         }
     }
-    __syncthreads();
+    consumers_sync();
     if (tid < 32) {
         int n = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
@@ -152,7 +178,7 @@ __device__ void few_route(const FewArgs &a, FewRouting &r) {
             r.ndrop = nu - n;
         }
     }
-    __syncthreads();
+    consumers_sync();
     if (blockIdx.x == 0) {  // the routing's optional outputs
         for (int s = tid; s < Tk; s += nthr) {
             if (a.idx) a.idx[s] = r.idx[s];
@@ -172,164 +198,616 @@ __device__ __forceinline__ float few_weight(const FewArgs &a, const FewRouting &
     return 0.f;
 }
 
-// Eight consecutive weights of row r from column k (a multiple of 8) of a [rows, K] matrix.
-template <int FMT>
-__device__ __forceinline__ void load8(const FewMatrix &m, size_t r, int K, int k, float (&v)[8]) {
-    if constexpr (FMT == 0) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(m.w) + r * K + k));
-        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-    } else if constexpr (FMT == 1) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(m.w) + r * K + k));
-        const int se = (int)m.sf[((r / 64 * (K / 128) + k / 128) * 64 + r % 64) * 4 + k % 128 / 32] - 127;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = bf16_bits_to_f32(quant::e4m3_scaled_bf16((uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3))), se));
-    } else {
-        const uint32_t q =
-            __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(m.w) + (r * K + k) / 2));
-        const uint8_t sc = m.sf[((r / 64 * (K / 128) + k / 128) * 64 + r % 64) * 8 + k % 128 / 16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = bf16_bits_to_f32(quant::nvfp4_scaled_bf16((uint8_t)((q >> (4 * i)) & 15u), sc));
-    }
-}
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+// ------------------------------------------------------------- the stream --
+// Shapes of a ring slot: 128 weight rows of kK columns, their block scales,
+// and up to 2 Tp token rows of kK bf16.
+template <int FMT, int NT>
+struct FewShape {
+    static constexpr int kTp = 8 * NT;               // token rows (T rounded up)
+    static constexpr int kK = FMT == 0 ? 64 : 128;   // K columns per chunk
+    static constexpr int kRowBytes = FMT == 2 ? 64 : 128;
+    static constexpr int kWBytes = 128 * kRowBytes;
+    static constexpr int kScaleBytes = FMT == 0 ? 0 : FMT == 1 ? 512 : 1024;
+    static constexpr int kBoxes = kK / 64;           // 64-column token boxes
+    static constexpr int kXBytes = kBoxes * kTp * 128;
+    static constexpr int kTokOff = kWBytes + 1024 * (FMT != 0);
+    static constexpr int kSlotBytes = kTokOff + 2 * kXBytes;
+    static constexpr int kPartFloats = 256 * NT * 4;  // one row block's sums: 8 warps x 32 lanes
+    static constexpr int kFixed = 1024 + (int)sizeof(FewRouting) + kPartFloats * 4 * 2 + 1024;
+    static constexpr int kSlots = (kFewSmem - kFixed) / kSlotBytes;
+    static constexpr int kSmem = 1024 + kSlots * kSlotBytes + kPartFloats * 4 * 2 + (int)sizeof(FewRouting) + 1024;
+};
+
+struct __align__(64) FewMaps {
+    CUtensorMap gate, up, down, s_gate, s_up, s_down, x, h;
+};
+
+struct FewPlan {
+    FewArgs a;
+    uint16_t *h;   // [2 Tp, ldh] bf16: h, then its remainder
+    int ldh;
+    float *part;   // [3][kFewMaxSms][2] row-block partials
+    int32_t *sync; // [0], [1] grid barriers, [2] CTAs done, [16 + phase * kFewMaxSms + cta] partial arrivals
+};
+
+// This CTA's share of a phase: chunks [lo, hi) of `total`, `per` to a row block.
+struct Share {
+    int per, total, ctas, lo, hi;
+    __device__ Share(int units, int per_unit) : per(per_unit), total(units * per_unit) {
+        ctas = min((int)gridDim.x, total);
+        lo = hi = 0;
+        if ((int)blockIdx.x < ctas) {
+            lo = (int)((long long)blockIdx.x * total / ctas);
+            hi = (int)((long long)(blockIdx.x + 1) * total / ctas);
+        }
+    }
+    // the CTA whose share holds chunk c
+    __device__ int owner(int c) const { return (int)(((long long)(c + 1) * ctas - 1) / total); }
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void lds64(uint32_t (&r)[2], uint32_t addr) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-
-// acc[t] += row r of m . x_t over K columns (x bf16 or fp32 [T, ldx]), this lane's share.
-template <int FMT, class X>
-__device__ __forceinline__ void row_dots(const FewMatrix &m, size_t r, int K, const X *x, size_t ldx, uint32_t tokens,
-                                         int lane, float (&acc)[kFewMaxTokens]) {
-    for (int k = lane * 8; k < K; k += 256) {
-        float w[8];
-        load8<FMT>(m, r, K, k, w);
-#pragma unroll
-        for (int t = 0; t < kFewMaxTokens; ++t)
-            if ((tokens >> t) & 1u)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float xv;
-                    if constexpr (sizeof(X) == 2)
-                        xv = bf16_bits_to_f32(x[t * ldx + k + i]);
-                    else
-                        xv = __ldcg(x + t * ldx + k + i);
-                    acc[t] = fmaf(w[i], xv, acc[t]);
-                }
-    }
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const FewArgs a) {
-    __shared__ FewRouting r;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int gw = blockIdx.x * kFewWarps + warp, nw = gridDim.x * kFewWarps;
-    const uint32_t all = (1u << a.T) - 1u;
-    float *h = static_cast<float *>(a.h);
-    if (a.project) {
-        const FewMatrix m{a.w_router, nullptr, nullptr};
-        for (int e = gw; e < a.E; e += nw) {
-            float acc[kFewMaxTokens] = {};
-            row_dots<0>(m, e, a.H, a.x, a.H, all, lane, acc);
+// Sixteen codes of one row as bf16 pairs times their block's scale, exactly.
+//
+// E4M3: the code's sign, exponent and mantissa moved to a bf16's fields are
+// the value times 2^-120 (subnormals included), so one bf16 product with
+// 2^(120 + se) finishes it; codes (2i, 2i + 1) of word j give pair 2j + i.
+// That factor is a bf16 while se <= 7 (weights below 2^16); larger scales take
+// the scalar decoder.
+__device__ __forceinline__ void decode16_mx(uint32_t (&v)[8], const uint32_t (&c)[4], uint32_t scale) {
+    if (__builtin_expect(scale <= 134u, 1)) {
+        const uint32_t f = (scale + 120u) * 0x00800080u;
 #pragma unroll
-            for (int t = 0; t < kFewMaxTokens; ++t)
-                if (t < a.T) {
-                    const float s = warp_sum(acc[t]);
-                    if (lane == 0) a.logits[(size_t)t * a.E + e] = s;
-                }
-        }
-        if (!grid_meet(a.sync, a.status, &r.stop)) return;
-    }
-    few_route(a, r);
-    if (a.Is > 0)
-        for (int t = gw; t < a.T; t += nw) {
-            float z = 0.f;
-            for (int i = lane; i < a.H; i += 32)
-                z = fmaf(bf16_bits_to_f32(a.x[(size_t)t * a.H + i]), bf16_bits_to_f32(a.gvec[i]), z);
-            z = warp_sum(z);
-            if (lane == 0) a.sgate[t] = 1.f / (1.f + expf(-z));
-        }
-    const int nu = r.nu, Kt = a.Is + nu * a.I;  // columns of h: shared first, then the experts in list order
-    for (int c = gw; c < Kt; c += nw) {
-        const bool sh = c < a.Is;
-        const int u = sh ? 0 : (c - a.Is) / a.I, i = sh ? c : (c - a.Is) % a.I;
-        const int e = sh ? 0 : r.list[u];
-        const uint32_t tokens = sh ? all : r.mask[e];
-        const FewMatrix &mg = sh ? a.s_gate : a.gate, &mu = sh ? a.s_up : a.up;
-        const size_t row = sh ? (size_t)i : (size_t)e * a.I + i;
-        float g[kFewMaxTokens] = {}, up[kFewMaxTokens] = {};
-        row_dots<FMT>(mg, row, a.H, a.x, a.H, tokens, lane, g);
-        row_dots<FMT>(mu, row, a.H, a.x, a.H, tokens, lane, up);
-        const float tg = FMT == 2 ? mg.ts[e] : 1.f, tu = FMT == 2 ? mu.ts[e] : 1.f;
-        const float td = FMT == 2 ? (sh ? a.s_down.ts[0] : a.down.ts[e]) : 1.f;
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int t = 0; t < kFewMaxTokens; ++t)
-            if (t < a.T) {
-                const float gs = warp_sum(g[t]) * tg, us = warp_sum(up[t]) * tu;
-                float v = 0.f;
-                if ((tokens >> t) & 1u) {
-                    v = gs / (1.f + expf(-gs)) * us * td;
-                    if (!sh) v *= few_weight(a, r, t, e);
-                }
-                if (lane == 0) h[(size_t)t * Kt + c] = v;
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t x = __byte_perm(c[j], 0, i ? 0x3424 : 0x1404);  // bytes to the high halves
+                v[2 * j + i] = mul_bf16x2(((x >> 4) & 0x07F007F0u) | (x & 0x80008000u), f);
             }
-    }
-    if (!grid_meet(a.sync + 1, a.status, &r.stop)) return;
-    for (int o = gw; o < a.H; o += nw) {
-        float acc[kFewMaxTokens] = {};
-        if (a.Is > 0) {
-            row_dots<FMT>(a.s_down, o, a.Is, h, Kt, all, lane, acc);
+    } else {
 #pragma unroll
-            for (int t = 0; t < kFewMaxTokens; ++t)
-                if (t < a.T) acc[t] *= __ldcg(a.sgate + t);
-        }
-        for (int u = 0; u < nu; ++u) {
-            const int e = r.list[u];
-            row_dots<FMT>(a.down, (size_t)e * a.H + o, a.I, h + a.Is + (size_t)u * a.I, Kt, r.mask[e], lane, acc);
-        }
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int t = 0; t < kFewMaxTokens; ++t)
-            if (t < a.T) {
-                const float s = warp_sum(acc[t]);
-                if (lane == 0) a.out[(size_t)t * a.H + o] = f32_to_bf16_bits(s);
-            }
+            for (int i = 0; i < 2; ++i)
+                v[2 * j + i] =
+                    quant::e4m3_scaled_bf16((uint8_t)(c[j] >> (16 * i)), (int)scale - 127) |
+                    (uint32_t)quant::e4m3_scaled_bf16((uint8_t)(c[j] >> (16 * i + 8)), (int)scale - 127) << 16;
     }
-    // the last CTA out leaves the counters at zero
+}
+// E2M1: likewise the value times 2^-126; the factor holds the E4M3 block scale
+// times 2^118, the missing 2^8 goes to the matrix scale.  Word j's pairs are
+// codes (i, i + 4), i = 0..3, so that one shift and mask extracts both.
+constexpr float kNvFix = 256.f;
+__device__ __forceinline__ void decode16_nv(uint32_t (&v)[8], const uint32_t (&c)[2], uint32_t scale) {
+    const float sb = quant::e4m3_decode((uint8_t)scale) * 0x1p118f;  // exact: 4 significant bits
+    const uint32_t f = __byte_perm(__float_as_uint(sb), 0, 0x3232);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t mag = i < 2 ? c[j] << (6 - 4 * i) : c[j] >> (4 * i - 6);
+            v[4 * j + i] = mul_bf16x2((mag & 0x01C001C0u) | ((c[j] << (12 - 4 * i)) & 0x80008000u), f);
+        }
+}
+
+template <int FMT, int NT>
+__global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewMaps maps, const FewPlan p) {
+    using S = FewShape<FMT, NT>;
+    constexpr int kTp = S::kTp, kSlots = S::kSlots;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *xch = reinterpret_cast<float *>(ring + (size_t)kSlots * S::kSlotBytes);  // group 1's sums; projection sums
+    FewRouting &r = *reinterpret_cast<FewRouting *>(xch + 2 * S::kPartFloats);
+    uint64_t *fullw = reinterpret_cast<uint64_t *>((reinterpret_cast<uintptr_t>(&r + 1) + 7) & ~uintptr_t(7));
+    uint64_t *fullb = fullw + kSlots, *empty = fullb + kSlots, *routed = empty + kSlots;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(routed + 1);
+    volatile int *last_flag = abort_flag + 1;
+    const FewArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&fullw[s], 1);
+            mbar_init(&fullb[s], 1);
+            mbar_init(&empty[s], kFewConsumers / 32);
+        }
+        mbar_init(routed, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
     __syncthreads();
-    if (threadIdx.x == 0 && atomicAdd(a.sync + 2, 1) == (int)gridDim.x - 1) {
-        a.sync[0] = 0;
-        a.sync[1] = 0;
-        a.sync[2] = 0;
+
+    const int kH = a.H / S::kK, kS = a.Is / S::kK, kI = a.I / S::kK;  // chunks along H, Is, I
+    // the three phases' shares; the routed ones are known once the tokens are routed
+    auto share = [&](int phase) {
+        return phase == 0 ? Share(a.Is / 64, kH) : phase == 1 ? Share(r.nu * (a.I / 64), kH)
+                                                              : Share(a.H / 128, kS + r.nu * kI);
+    };
+
+    if (warp == kFewConsumers / 32) {
+        // ================= weight producer =================
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_first();
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int phase = 0; ok && phase < 3; ++phase) {
+                if (phase == 1 && !mbar_wait(routed, 0, abort_flag, a.status, true)) break;
+                const Share sh = share(phase);
+                int unit = sh.lo / max(sh.per, 1), kc = sh.lo - unit * sh.per;
+                for (int c = sh.lo; ok && c < sh.hi; ++c) {
+                    const uint32_t st = issued % kSlots, use = issued / kSlots;
+                    if (use > 0 && !mbar_wait_fast(&empty[st], (use - 1) & 1u, abort_flag, a.status, true)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *dst = ring + (size_t)st * S::kSlotBytes;
+                    mbar_arrive_expect_tx(&fullw[st], S::kWBytes + S::kScaleBytes);
+                    const CUtensorMap *m0, *m1;
+                    const uint8_t *f0, *f1;  // packed scales of the two 64-row halves
+                    int x, y0, y1, kcol, cols;
+                    if (phase < 2) {
+                        const int per = a.I / 64, e = phase ? r.list[unit / per] : 0;
+                        m0 = phase ? &maps.gate : &maps.s_gate;
+                        m1 = phase ? &maps.up : &maps.s_up;
+                        f0 = phase ? a.gate.sf : a.s_gate.sf;
+                        f1 = phase ? a.up.sf : a.s_up.sf;
+                        kcol = kc;
+                        cols = kH;
+                        y0 = y1 = phase ? e * a.I + unit % per * 64 : unit * 64;
+                    } else {
+                        const bool shared = kc < kS;
+                        const int u = shared ? 0 : (kc - kS) / kI;
+                        m0 = m1 = shared ? &maps.s_down : &maps.down;
+                        f0 = f1 = shared ? a.s_down.sf : a.down.sf;
+                        kcol = shared ? kc : kc - kS - u * kI;
+                        cols = shared ? kS : kI;
+                        y0 = unit * 128 + (shared ? 0 : r.list[u] * a.H);
+                        y1 = y0 + 64;
+                    }
+                    x = kcol * (FMT == 0 ? 64 : S::kRowBytes);
+                    tma_load_2d_hint(m0, &fullw[st], dst, x, y0, pol);
+                    tma_load_2d_hint(m1, &fullw[st], dst + S::kWBytes / 2, x, y1, pol);
+                    if constexpr (FMT != 0) {
+                        constexpr int kRun = S::kScaleBytes / 2;
+                        bulk_load(dst + S::kWBytes, f0 + ((size_t)(y0 / 64) * cols + kcol) * kRun, kRun, &fullw[st]);
+                        bulk_load(dst + S::kWBytes + kRun, f1 + ((size_t)(y1 / 64) * cols + kcol) * kRun, kRun,
+                                  &fullw[st]);
+                    }
+                    ++issued;
+                    if (++kc == sh.per) {
+                        kc = 0;
+                        ++unit;
+                    }
+                }
+            }
+            for (uint32_t n = issued > (uint32_t)kSlots ? issued - kSlots : 0; n < issued; ++n)  // copies in flight
+                mbar_wait(&fullw[n % kSlots], (n / kSlots) & 1u, abort_flag, a.status, false);
+        }
+    } else if (warp == kFewConsumers / 32 + 1) {
+        // ================= token producer =================
+        if (lane == 0) {
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int phase = 0; ok && phase < 3; ++phase) {
+                if (phase == 1 && !mbar_wait(routed, 0, abort_flag, a.status, true)) break;
+                const Share sh = share(phase);
+                if (phase == 2) {
+                    if (!grid_wait(p.sync + 1, abort_flag, a.status)) break;
+                    fence_proxy_async_global();  // h was written by ordinary stores
+                }
+                int kc = sh.lo % max(sh.per, 1);
+                for (int c = sh.lo; ok && c < sh.hi; ++c) {
+                    const uint32_t st = issued % kSlots, use = issued / kSlots;
+                    if (use > 0 && !mbar_wait_fast(&empty[st], (use - 1) & 1u, abort_flag, a.status, true)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *dst = ring + (size_t)st * S::kSlotBytes + S::kTokOff;
+                    const int rows = phase == 2 ? 2 : 1;
+                    mbar_arrive_expect_tx(&fullb[st], rows * S::kXBytes);
+#pragma unroll
+                    for (int b = 0; b < S::kBoxes; ++b)
+                        tma_load_2d(phase == 2 ? &maps.h : &maps.x, &fullb[st], dst + b * rows * kTp * 128,
+                                    kc * S::kK + b * 64, 0);
+                    ++issued;
+                    if (++kc == sh.per) kc = 0;
+                }
+            }
+            for (uint32_t n = issued > (uint32_t)kSlots ? issued - kSlots : 0; n < issued; ++n)
+                mbar_wait(&fullb[n % kSlots], (n / kSlots) & 1u, abort_flag, a.status, false);
+        }
+    } else {
+        // ================= consumers =================
+        const int tid = threadIdx.x;
+        // the shared expert's gate, one token per CTA from the grid's end
+        const int gt = (int)gridDim.x - 1 - cta;
+        if (a.Is > 0)
+            for (int t = gt; t < a.T; t += gridDim.x) {
+                float z = 0.f;
+                for (int i = tid; i < a.H / 8; i += kFewConsumers) {
+                    const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.H) + i);
+                    const uint4 gv = __ldg(reinterpret_cast<const uint4 *>(a.gvec) + i);
+                    const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w}, gs[4] = {gv.x, gv.y, gv.z, gv.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        z = fmaf(__uint_as_float(xs[q] << 16), __uint_as_float(gs[q] << 16), z);
+                        z = fmaf(__uint_as_float(xs[q] & 0xffff0000u), __uint_as_float(gs[q] & 0xffff0000u), z);
+                    }
+                }
+#pragma unroll
+                for (int off = 16; off; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+                if (lane == 0) xch[warp] = z;
+                consumers_sync();
+                if (tid == 0) {
+                    z = 0.f;
+                    for (int w = 0; w < kFewConsumers / 32; ++w) z += xch[w];
+                    a.sgate[t] = 1.f / (1.f + expf(-z));
+                }
+                consumers_sync();
+            }
+        if (a.project) {
+            // logits: eight experts (the mma's columns) per CTA, tokens its rows, the
+            // warps on alternate 64-wide K blocks; lane (g, q) holds 16 consecutive
+            // columns 16 q of rows g and g + 8, the same permutation of K on both sides
+            const int g = lane >> 2, q = lane & 3;
+            for (int o = cta; o < (a.E + 7) / 8; o += gridDim.x) {
+                const uint16_t *x0 = a.x + (size_t)min(g, a.T - 1) * a.H, *x1 = a.x + (size_t)min(g + 8, a.T - 1) * a.H;
+                const uint16_t *w0 = a.w_router + (size_t)min(o * 8 + g, a.E - 1) * a.H;
+                float d[4] = {};
+#pragma unroll 3
+                for (int kb = warp; kb < a.H / 64; kb += kFewConsumers / 32) {
+                    const int k = kb * 64 + q * 16;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(x0 + k) + i);
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x1 + k) + i);
+                        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(w0 + k) + i);
+                        mma16816(d, u.x, v.x, u.y, v.y, w.x, w.y);
+                        mma16816(d, u.z, v.z, u.w, v.w, w.z, w.w);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xch[warp * 128 + (g + 8 * (i >> 1)) * 8 + 2 * q + (i & 1)] = d[i];
+                consumers_sync();
+                if (tid < 128) {
+                    float v = 0.f;
+                    for (int w = 0; w < kFewConsumers / 32; ++w) v += xch[w * 128 + tid];
+                    const int t = tid >> 3, e = o * 8 + (tid & 7);
+                    if (t < a.T && e < a.E) a.logits[(size_t)t * a.E + e] = v;
+                }
+                consumers_sync();
+            }
+            if (tid == 0) {
+                grid_arrive(p.sync);
+                grid_wait(p.sync, abort_flag, a.status);
+            }
+            consumers_sync();
+        }
+        few_route(a, r);
+        if (tid == 0) mbar_arrive(routed);
+
+        const int grp = warp >> 3, wr = warp & 7, g = lane >> 2, q = lane & 3;
+        bool dead = false;  // a wait gave up: go through the motions to the end
+        uint32_t used = 0;
+        float sg[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sg[n][0] = sg[n][1] = 0.f;
+        for (int phase = 0; phase < 3; ++phase) {
+            const Share sh = share(phase);
+            int unit = sh.lo / max(sh.per, 1), kc = sh.lo - unit * sh.per, left = sh.hi - sh.lo;
+            bool have_sg = false;
+            while (left > 0) {
+                const int n_chunks = min(sh.per - kc, left);
+                float acc[NT][4] = {};
+                auto scale_shared = [&] {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        acc[n][0] *= sg[n][0];
+                        acc[n][1] *= sg[n][1];
+                        acc[n][2] *= sg[n][0];
+                        acc[n][3] *= sg[n][1];
+                    }
+                };
+                for (int i = 0; i < n_chunks; ++i, ++used) {
+                    const uint32_t st = used % kSlots, ph = (used / kSlots) & 1u;
+                    if (!dead) dead = !mbar_wait_fast(&fullw[st], ph, abort_flag, a.status, true);
+                    if (!dead) dead = !mbar_wait_fast(&fullb[st], ph, abort_flag, a.status, true);
+                    if (phase == 2 && !have_sg) {  // the token operand is past the grid barrier: so are the gates
+                        have_sg = true;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const int t = n * 8 + 2 * q + c;
+                                sg[n][c] = a.Is > 0 && t < a.T ? __ldcg(a.sgate + t) : 0.f;
+                            }
+                    }
+                    // the shared expert's channels come first: their sum takes the gate before the routed ones join
+                    if (phase == 2 && kc + i == kS && i > 0) scale_shared();
+                    const uint32_t wb = smem_u32(ring + (size_t)st * S::kSlotBytes), tb = wb + S::kTokOff;
+                    // rows 0..7 and 8..15 of this warp's tile within the slot
+                    const uint32_t r0 = phase < 2 ? wr * 8 : wr * 16, r1 = phase < 2 ? 64 + wr * 8 : wr * 16 + 8;
+                    if constexpr (FMT == 0) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {  // this group's two of the four K16 steps
+                            const int ks = grp * 2 + s, mi = lane >> 3, lr = lane & 7;
+                            uint32_t A[4];
+                            ldsm4(A, wb + ((mi & 1 ? r1 : r0) + lr) * 128 + (((2 * ks + (mi >> 1)) ^ lr) << 4));
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                // matrices 0, 1: h (or x), 2, 3: its remainder
+                                uint32_t B[4];
+                                const uint32_t row = n * 8 + lr + (phase == 2 && mi >= 2 ? kTp : 0);
+                                ldsm4(B, tb + row * 128 + (((2 * ks + (mi & 1)) ^ lr) << 4));
+                                mma16816(acc[n], A[0], A[1], A[2], A[3], B[0], B[1]);
+                                if (phase == 2) mma16816(acc[n], A[0], A[1], A[2], A[3], B[2], B[3]);
+                            }
+                        }
+                    } else {
+                        // this group's 64 of the 128 columns: lane (g, q) takes 16 codes of rows
+                        // g and g + 8 (one block scale each) and the same 16 token columns
+                        uint32_t v0[8], v1[8];
+                        const uint32_t ra = r0 + g, rb = r1 + g;
+                        if constexpr (FMT == 1) {
+                            uint32_t c0[4], c1[4];
+                            lds128(c0, wb + ra * 128 + (((grp * 4 + q) ^ (ra & 7)) << 4));
+                            lds128(c1, wb + rb * 128 + (((grp * 4 + q) ^ (rb & 7)) << 4));
+                            const uint32_t sc = wb + S::kWBytes + grp * 2 + (q >> 1);
+                            decode16_mx(v0, c0, lds8(sc + ra * 4));
+                            decode16_mx(v1, c1, lds8(sc + rb * 4));
+                        } else {
+                            uint32_t c0[2], c1[2];
+                            const uint32_t un = grp * 2 + (q >> 1), in = (q & 1) * 8;
+                            lds64(c0, wb + ra * 64 + ((un ^ ((ra >> 1) & 3)) << 4) + in);
+                            lds64(c1, wb + rb * 64 + ((un ^ ((rb >> 1) & 3)) << 4) + in);
+                            const uint32_t sc = wb + S::kWBytes + grp * 4 + q;
+                            decode16_nv(v0, c0, lds8(sc + ra * 8));
+                            decode16_nv(v1, c1, lds8(sc + rb * 8));
+                        }
+                        const int parts = phase == 2 ? 2 : 1;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                if (part == 1 && phase != 2) break;
+                                const uint32_t row = tb + (uint32_t)(grp * parts * kTp + part * kTp + n * 8 + g) * 128;
+                                uint32_t b[8];
+                                lds128(reinterpret_cast<uint32_t(&)[4]>(b[0]), row + (((2 * q) ^ g) << 4));
+                                lds128(reinterpret_cast<uint32_t(&)[4]>(b[4]), row + (((2 * q + 1) ^ g) << 4));
+#pragma unroll
+                                for (int s = 0; s < 4; ++s) {
+                                    uint32_t b0 = b[2 * s], b1 = b[2 * s + 1];
+                                    if constexpr (FMT == 2) {  // the columns in the codes' pair order
+                                        const uint32_t lo = b[(s >> 1) * 4 + (s & 1)], hi = b[(s >> 1) * 4 + (s & 1) + 2];
+                                        b0 = __byte_perm(lo, hi, 0x5410);
+                                        b1 = __byte_perm(lo, hi, 0x7632);
+                                    }
+                                    mma16816(acc[n], v0[2 * s], v1[2 * s], v0[2 * s + 1], v1[2 * s + 1], b0, b1);
+                                }
+                            }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[st]);
+                }
+                if (phase == 2 && kc < kS && kc + n_chunks <= kS) scale_shared();  // the shared part alone
+                // both groups' sums
+                if (grp == 1) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        *reinterpret_cast<float4 *>(xch + (n * 256 + wr * 32 + lane) * 4) =
+                            make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                }
+                named_bar_sync(2, kFewConsumers);
+                if (grp == 0) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float4 o = *reinterpret_cast<const float4 *>(xch + (n * 256 + wr * 32 + lane) * 4);
+                        acc[n][0] += o.x;
+                        acc[n][1] += o.y;
+                        acc[n][2] += o.z;
+                        acc[n][3] += o.w;
+                    }
+                }
+                named_bar_sync(3, kFewConsumers);
+                if (grp == 0) {
+                    bool whole = n_chunks == sh.per;
+                    if (!whole) {
+                        // a row block shared with other CTAs: the last to arrive adds the partials
+                        const int first = sh.owner(unit * sh.per), last = sh.owner(unit * sh.per + sh.per - 1);
+                        auto slot = [&](int c) {
+                            return reinterpret_cast<float4 *>(
+                                       p.part + (size_t)((phase * kFewMaxSms + c) * 2 + (c == first)) * S::kPartFloats) +
+                                   wr * 32 + lane;
+                        };
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            __stcg(slot(cta) + n * 256, make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]));
+                        __threadfence();
+                        named_bar_sync(4, 256);
+                        if (tid == 0) {
+                            int32_t *ctr = p.sync + 16 + phase * kFewMaxSms + first;
+                            const bool is_last = atomicAdd(ctr, 1) == last - first;
+                            if (is_last) *ctr = 0;
+                            __threadfence();
+                            *last_flag = is_last;
+                        }
+                        named_bar_sync(4, 256);
+                        whole = *last_flag != 0;
+                        if (whole) {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+                            for (int c = first; c <= last; ++c)
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    const float4 o = __ldcg(slot(c) + n * 256);
+                                    acc[n][0] += o.x;
+                                    acc[n][1] += o.y;
+                                    acc[n][2] += o.z;
+                                    acc[n][3] += o.w;
+                                }
+                        }
+                    }
+                    if (whole && phase < 2) {
+                        // gate (rows 0..7) and up (8..15) of one channel are in one thread
+                        const int per = a.I / 64, u = phase ? unit / per : 0, e = phase ? r.list[u] : 0;
+                        const int ch = (phase ? unit % per : unit) * 64 + wr * 8 + g;
+                        const uint32_t tokens = phase ? r.mask[e] : (1u << a.T) - 1u;
+                        uint16_t *dst = p.h + (phase ? a.Is + (size_t)u * a.I : 0) + ch;
+                        float tg = 1.f, tu = 1.f, td = 1.f;
+                        if constexpr (FMT == 2) {
+                            tg = kNvFix * __ldg((phase ? a.gate.ts : a.s_gate.ts) + e);
+                            tu = kNvFix * __ldg((phase ? a.up.ts : a.s_up.ts) + e);
+                            td = kNvFix * __ldg((phase ? a.down.ts : a.s_down.ts) + e);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const int t = n * 8 + 2 * q + c;
+                                float v = 0.f;
+                                if ((tokens >> t) & 1u) {
+                                    const float gv = acc[n][c] * tg;
+                                    v = gv / (1.f + expf(-gv)) * (acc[n][2 + c] * tu) * td;
+                                    if (phase) v *= few_weight(a, r, t, e);
+                                }
+                                const uint16_t hi = f32_to_bf16_bits(v);
+                                const float rem = v - bf16_bits_to_f32(hi);
+                                dst[(size_t)t * p.ldh] = hi;
+                                // an infinite or NaN h has no remainder
+                                dst[(size_t)(kTp + t) * p.ldh] = f32_to_bf16_bits(fabsf(rem) < INFINITY ? rem : 0.f);
+                            }
+                    } else if (whole) {
+                        const int o = unit * 128 + wr * 16 + g;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const int t = n * 8 + 2 * q + (c & 1);
+                                if (t < a.T) a.out[(size_t)t * a.H + o + (c >> 1) * 8] = f32_to_bf16_bits(acc[n][c]);
+                            }
+                    }
+                }
+                left -= n_chunks;
+                kc = 0;
+                ++unit;
+            }
+            if (phase == 1 && grp == 0) {  // this CTA's part of h is written
+                fence_proxy_async_global();
+                __threadfence();
+                named_bar_sync(4, 256);
+                if (tid == 0) grid_arrive(p.sync + 1);
+            }
+        }
+    }
+    // the last CTA out leaves the barriers at zero
+    __syncthreads();
+    if (threadIdx.x == 0 && atomicAdd(p.sync + 2, 1) == (int)gridDim.x - 1) {
+        p.sync[0] = 0;
+        p.sync[1] = 0;
+        p.sync[2] = 0;
     }
 }
 
+size_t part_bytes(int tp) { return (size_t)3 * kFewMaxSms * 2 * 128 * tp * 4; }
+int few_ldh(int T, int E, int I, int k, int Is) { return Is + std::min(E, T * k) * I; }
+int few_tp(int T) { return T <= 8 ? 8 : 16; }
+
 template <int FMT>
-cudaError_t launch_fmt(const FewArgs &a, cudaStream_t st) {
+bool encode_weights(CUtensorMap *m, const void *base, uint64_t rows, uint64_t K) {
+    if (FMT == 0) return encode_2d(m, base, rows, K, 64);
+    return FMT == 1 ? encode_2d_u8(m, base, rows, K, 64, 128) : encode_2d_u8(m, base, rows, K / 2, 64, 64);
+}
+
+template <int FMT, int NT>
+cudaError_t launch_shape(const FewArgs &a, cudaStream_t st) {
+    using S = FewShape<FMT, NT>;
+    static_assert(S::kSlots >= 4 && S::kSmem <= kFewSmem, "ring");
+    static_assert(S::kSlotBytes % 1024 == 0, "swizzled boxes need 1024-byte aligned slots");
+    FewMaps m;
+    const uint64_t E = a.E, I = a.I, H = a.H, Is = a.Is;
+    FewPlan p;
+    p.a = a;
+    p.ldh = few_ldh(a.T, a.E, a.I, a.k, a.Is);
+    p.part = static_cast<float *>(a.h);
+    p.h = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(a.h) + part_bytes(S::kTp));
+    p.sync = a.sync;
+    if (!encode_weights<FMT>(&m.gate, a.gate.w, E * I, H) || !encode_weights<FMT>(&m.up, a.up.w, E * I, H) ||
+        !encode_weights<FMT>(&m.down, a.down.w, E * H, I) || !encode_2d(&m.x, a.x, a.T, H, S::kTp) ||
+        !encode_2d(&m.h, p.h, 2 * S::kTp, p.ldh, 2 * S::kTp))
+        return cudaErrorInvalidValue;
+    if (Is > 0) {
+        if (!encode_weights<FMT>(&m.s_gate, a.s_gate.w, Is, H) || !encode_weights<FMT>(&m.s_up, a.s_up.w, Is, H) ||
+            !encode_weights<FMT>(&m.s_down, a.s_down.w, H, Is))
+            return cudaErrorInvalidValue;
+    } else {
+        m.s_gate = m.s_up = m.s_down = m.gate;  // not read
+    }
+    static std::atomic<int> attr_set[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(few_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(1, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(device_sm_count());
+    cfg.gridDim = dim3(std::min(device_sm_count(), kFewMaxSms));
     cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, few_kernel<FMT>, a);
+    return cudaLaunchKernelEx(&cfg, few_kernel<FMT, NT>, m, p);
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const FewArgs &a, cudaStream_t st) {
+    return a.T <= 8 ? launch_shape<FMT, 1>(a, st) : launch_shape<FMT, 2>(a, st);
 }
 
 }  // namespace
 
-size_t few_h_bytes(int T, int E, int I, int k, int Is) {
-    const size_t used = (size_t)std::min(E, T * k);
-    return (size_t)kFewMaxTokens * (used * I + Is) * 4;
+size_t few_scratch_bytes(int T, int E, int I, int k, int Is) {
+    const int tp = few_tp(T);
+    return part_bytes(tp) + (size_t)2 * tp * few_ldh(T, E, I, k, Is) * 2;
 }
 
 cudaError_t launch_few(const FewArgs &a, int fmt, cudaStream_t st) {

@@ -30,13 +30,13 @@ struct FewArgs {
     uint8_t *kept;
     int32_t *n_dropped;
     uint16_t *out;
-    void *h;        // gate/up activations
+    void *h;        // scratch: row-block partials, then the gate/up activations
     int32_t *status, *sync;
 };
 
 // Ints of the workspace head the kernel's counters take (zero between launches).
-constexpr int kFewSyncInts = 16;
-size_t few_h_bytes(int T, int E, int I, int k, int Is);
+constexpr int kFewSyncInts = 16 + 3 * 160;
+size_t few_scratch_bytes(int T, int E, int I, int k, int Is);
 // fmt: 0 bf16, 1 MXFP8, 2 NVFP4.
 cudaError_t launch_few(const FewArgs &a, int fmt, cudaStream_t st);
 

@@ -60,7 +60,7 @@ WsLayout ws_layout(const moe_config_t &c, int T) {
     L.logits = take((size_t)T * E * 4);
     L.rpart = take(rp_partial_bytes(T, (int)E, c.hidden));
     L.few = T <= kFewMaxTokens
-                ? take(few_h_bytes(T, (int)E, c.moe_intermediate_size, c.num_experts_per_tok,
+                ? take(few_scratch_bytes(T, (int)E, c.moe_intermediate_size, c.num_experts_per_tok,
                                    c.shared_intermediate_size))
                 : off;
     L.total = off;
