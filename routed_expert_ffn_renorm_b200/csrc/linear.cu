@@ -1,53 +1,468 @@
-// The fused linear map out = residual + act(x W^T + bias): bf16 operands,
-// fp32 sums, one rounding of the result (or none, fp32 out).
+// The fused linear map out = residual + act(x W^T + bias) on the
+// 5th-generation tensor cores: bf16 operands, fp32 sums, one rounding of the
+// result (or none, fp32 out).
 //
-// One 64 x 64 output tile per CTA from 16-wide K slices in shared memory,
-// 4 x 4 outputs per thread.
+// One kernel from one token to long prompts.  The MMA's M is output channels
+// and its N tokens: a tile is 128 rows of W (256 for a CTA pair, 128 in each
+// CTA) by Nt tokens, Nt the tokens rounded up to 16 (at most 256 a tile), so
+// that a few tokens pay for a few columns and not for a padded row block.  K
+// runs in 64-wide slices, both operands TMA-loaded into 128-byte-swizzled
+// shared memory; ragged edges are zero-filled by TMA and not stored.  The fp32
+// accumulator lives in TMEM, double buffered: a tile's epilogue runs under the
+// next one's products.
+//
+// Bound: few tokens stream W from HBM (one CTA per SM, single tiles); from
+// about 200 tokens on the tensor cores bind, and a pair halves each CTA's share
+// of the token operand.
+//
+// Tiles go to the grid in whole waves, in bands of 8 row tiles so that a wave's
+// operands stay in L2; the tiles that would make up a last, partial wave have
+// their K range cut into equal contiguous shares over the whole grid.  Shares of
+// a tile leave fp32 partials in the workspace, and the last CTA to arrive adds
+// them in share order: the same bits on every run, and nobody waits.
+//
+// Roles: warp 0 TMA producer (one lane), warp 1 TMEM allocation and MMA issue
+// (one lane), warps 2..9 epilogue (two to each TMEM lane quarter, on alternate
+// 32-column blocks).  A lane holds one output channel, so a warp's store of one
+// token covers 32 consecutive channels.  Every wait is bounded: past the limit
+// the kernel sets MOE_STATUS_TIMEOUT and every role stops.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
 #include "linear.cuh"
+#include "tc_common.cuh"
 
 namespace moe {
 
 namespace {
+using namespace tc;
 
-constexpr int kTile = 64, kSlice = 16;
+constexpr int kLinThreads = 320;
+constexpr int kLinEpi = 256;
+constexpr int kLinMaxSms = 160;                // no device has more SMs (workspace sizing)
+constexpr int kLinSliceA = 128 * 128;          // 128 rows of W x 64 columns
+constexpr int kLinRing = 216 * 1024;           // at most
+constexpr int kLinAccStride = 256;             // TMEM columns between the two accumulators
+constexpr int kLinBand = 8;                    // row tiles of a band
+constexpr int kLinMaxStages = 16;
 
-__global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a) {
-    __shared__ float xs[kSlice][kTile + 1], wsh[kSlice][kTile + 1];
-    const int t0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += kSlice) {
-        for (int i = threadIdx.x; i < kTile * kSlice; i += 256) {
-            const int r = i / kSlice, c = i % kSlice, k = k0 + c;
-            xs[c][r] = t0 + r < a.T && k < a.K ? bf16_bits_to_f32(a.x[(size_t)(t0 + r) * a.K + k]) : 0.f;
-            wsh[c][r] = n0 + r < a.N && k < a.K ? bf16_bits_to_f32(a.w[(size_t)(n0 + r) * a.K + k]) : 0.f;
+struct __align__(64) LinMaps {
+    CUtensorMap w;  // [N, K], box 64 x 128
+    CUtensorMap x;  // [T, K], box 64 x Nt (pair: Nt / 2)
+};
+
+struct LinPlan {
+    LinearArgs a;
+    int Nt, nk;         // tokens of a tile (the MMA's N), K slices
+    int rt, tt;         // row tiles, token tiles
+    int waves;          // whole waves of tiles
+    int rest, sharers;  // tiles left, workers that share their K slices (== rest: a tile each)
+    int stages;
+};
+
+// The tiles of worker w (a CTA or a pair): its tile of every wave, then its share of the rest.
+struct LinWalk {
+    int w, workers, nk, waves, i, lo, hi, base;
+    __device__ LinWalk(const LinPlan &p, int worker, int n) : w(worker), workers(n), nk(p.nk), waves(p.waves), i(0) {
+        base = waves * workers;
+        lo = hi = 0;
+        if (w < p.sharers) {
+            const long long total = (long long)p.rest * nk;
+            lo = (int)(w * total / p.sharers);
+            hi = (int)((w + 1) * total / p.sharers);
         }
-        __syncthreads();
+    }
+    __device__ bool next(int &tile, int &k0, int &k1) {
+        if (i < waves) {
+            tile = i * workers + w;
+            k0 = 0;
+            k1 = nk;
+            ++i;
+            return true;
+        }
+        if (lo >= hi) return false;
+        const int t = lo / nk;
+        tile = base + t;
+        k0 = lo - t * nk;
+        k1 = min(nk, k0 + hi - lo);
+        lo += k1 - k0;
+        return true;
+    }
+};
+
+__device__ __forceinline__ void lin_tile(const LinPlan &p, int tile, int &r, int &j) {
+    const int band = tile / (kLinBand * p.tt), in = tile - band * kLinBand * p.tt;
+    const int rows = min(kLinBand, p.rt - band * kLinBand);
+    j = in / rows;
+    r = band * kLinBand + in - j * rows;
+}
+
+// Channel n of tokens t0 .. t0 + count - 1 from the sums v: everything in fp32, rounded once.
+__device__ __forceinline__ void lin_store32(const LinearArgs &a, int t0, int count, int n, float bias, float (&v)[32]) {
+    const size_t o = (size_t)t0 * a.N + n;
+    float res[32];
 #pragma unroll
-        for (int c = 0; c < kSlice; ++c)
+    for (int i = 0; i < 32; ++i) res[i] = 0.f;
+    if (a.residual) {  // all read before the first store: out may be the residual
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[c][ty * 4 + i], wsh[c][tx + 16 * j], acc[i][j]);
-        __syncthreads();
+        for (int i = 0; i < 32; ++i)
+            if (i < count) res[i] = bf16_bits_to_f32(a.residual[o + (size_t)i * a.N]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 32; ++i) v[i] += bias;
+    if (a.act == MOE_ACT_RELU) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int t = t0 + ty * 4 + i, n = n0 + tx + 16 * j;
-            if (t < a.T && n < a.N) linear_store(a, t, n, acc[i][j]);
+        for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_RELU>(v[i]);
+    } else if (a.act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_GELU>(v[i]);
+    } else if (a.act == MOE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_SILU>(v[i]);
+    }
+    if (a.out_f32) {
+        float *out = static_cast<float *>(a.out) + o;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < count) out[(size_t)i * a.N] = v[i] + res[i];
+    } else {
+        uint16_t *out = static_cast<uint16_t *>(a.out) + o;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < count) out[(size_t)i * a.N] = f32_to_bf16_bits(v[i] + res[i]);
+    }
+}
+
+template <bool kPair>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinPlan p) {
+    constexpr int kSlices = kPair ? 1 : 2;  // K slices per stage: one barrier round trip for two small ones
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t full[kLinMaxStages], empty[kLinMaxStages], tfull[2], tempty[2], mma_done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag, go_flag, last_flag;
+    const LinearArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+    const int worker = kPair ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+    const int workers = kPair ? (int)gridDim.x >> 1 : (int)gridDim.x;
+    const uint32_t brows = kPair ? (uint32_t)p.Nt >> 1 : (uint32_t)p.Nt;  // token rows this CTA loads
+    const uint32_t slice = kLinSliceA + (brows * 128 + 1023) / 1024 * 1024;
+    const uint32_t slice_tx = kLinSliceA + brows * 128;
+    pdl_launch_dependents();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], kPair ? 2 : 1);
+        }
+        mbar_init(&mma_done, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&maps.w);
+        prefetch_tmap(&maps.x);
+    }
+    if (warp == 1) {
+        if constexpr (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                         "r"(2 * kLinAccStride)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                         "r"(2 * kLinAccStride)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+        tc_fence_before();
+    }
+    if constexpr (kPair) cluster_sync();  // the other CTA's barriers exist before anything arrives on them
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = tmem_slot;
+    pdl_wait();  // the operands and the workspace are ready past this point
+
+    int tile, k0, k1;
+    if (warp == 0) {
+        // ================= TMA producer =================
+        if (lane == 0) {
+            // few tokens: every weight is read once.  Otherwise the bands' repeats hit L2
+            const uint64_t wpol = p.tt == 1 ? policy_evict_first() : policy_evict_normal();
+            const uint64_t xpol = policy_evict_normal();
+            LinWalk walk(p, worker, workers);
+            uint32_t issued = 0, ph = 0;
+            int st = 0;
+            bool ok = true;
+            while (ok && walk.next(tile, k0, k1)) {
+                int r, j;
+                lin_tile(p, tile, r, j);
+                const int wrow = kPair ? r * 256 + (int)rank * 128 : r * 128;
+                const int xrow = j * p.Nt + (int)(rank * brows);
+                for (int k = k0; k < k1; k += kSlices) {
+                    const int n = min(kSlices, k1 - k);
+                    if (issued >= (uint32_t)p.stages &&
+                        !mbar_wait_fast<kPair>(&empty[st], ph ^ 1u, &abort_flag, a.status, true)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *dst = ring + (size_t)st * kSlices * slice;
+                    if constexpr (kPair) {  // both CTAs' copies complete on CTA 0's barrier
+                        if (rank == 0) mbar_arrive_expect_tx(&full[st], 2u * slice_tx);
+                        const uint32_t bar0 = mapa(smem_u32(&full[st]), 0);
+                        tma_load_2d_pair(&maps.w, bar0, dst, k * 64, wrow, wpol);
+                        tma_load_2d_pair(&maps.x, bar0, dst + kLinSliceA, k * 64, xrow, xpol);
+                    } else {
+                        mbar_arrive_expect_tx(&full[st], (uint32_t)n * slice_tx);
+                        for (int u = 0; u < n; ++u) {
+                            tma_load_2d_hint(&maps.w, &full[st], dst + u * slice, (k + u) * 64, wrow, wpol);
+                            tma_load_2d(&maps.x, &full[st], dst + u * slice + kLinSliceA, (k + u) * 64, xrow);
+                        }
+                    }
+                    ++issued;
+                    if (++st == p.stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            // the copies still in flight (pair: released by the MMAs that read them)
+            for (uint32_t n = issued > (uint32_t)p.stages ? issued - p.stages : 0; n < issued; ++n) {
+                if constexpr (kPair)
+                    mbar_wait<true>(&empty[n % p.stages], (n / p.stages) & 1u, &abort_flag, a.status, false);
+                else
+                    mbar_wait(&full[n % p.stages], (n / p.stages) & 1u, &abort_flag, a.status, false);
+            }
+        }
+    } else if (warp == 1) {
+        // ================= MMA issuer =================
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = idesc_bf16(p.Nt, kPair ? 256 : 128);
+            const uint64_t desc0 = sw128_desc(smem_u32(ring));
+            LinWalk walk(p, worker, workers);
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (uint32_t it = 0; ok && walk.next(tile, k0, k1); ++it) {
+                const uint32_t acc = it & 1u;
+                if (!mbar_wait_fast<kPair>(&tempty[acc], ((it >> 1) & 1u) ^ 1u, &abort_flag, a.status, true)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + acc * kLinAccStride;
+                for (int k = k0; k < k1; k += kSlices) {
+                    const int n = min(kSlices, k1 - k);
+                    if (!mbar_wait_fast<kPair>(&full[st], ph, &abort_flag, a.status, true)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    for (int u = 0; u < n; ++u) {
+                        const uint64_t da = desc0 + (uint64_t)((st * kSlices + u) * slice / 16);
+                        const uint64_t db = da + kLinSliceA / 16;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {  // K16 steps: 32 bytes each
+                            if constexpr (kPair)
+                                umma_bf16_pair(d, da + 2 * kk, db + 2 * kk, idesc, k + u > k0 || kk > 0);
+                            else
+                                umma_bf16(d, da + 2 * kk, db + 2 * kk, idesc, k + u > k0 || kk > 0);
+                        }
+                    }
+                    if constexpr (kPair) umma_commit_pair(&empty[st]);
+                    else umma_commit(&empty[st]);
+                    if (++st == p.stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if constexpr (kPair) umma_commit_pair(&tfull[acc]);
+                else umma_commit(&tfull[acc]);
+            }
+            if constexpr (kPair) umma_commit_pair_local(&mma_done);
+            else umma_commit(&mma_done);
+            mbar_wait(&mma_done, 0, &abort_flag, a.status, false);
+        }
+    } else {
+        // ================= epilogue =================
+        const int q = warp & 3, half = (warp - 2) >> 2, row = q * 32 + lane;
+        const bool elected = threadIdx.x == 64;
+        auto release = [&](uint32_t acc) {
+            if (kPair && rank != 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
+            else mbar_arrive(&tempty[acc]);
+        };
+        LinWalk walk(p, worker, workers);
+        for (uint32_t it = 0; walk.next(tile, k0, k1); ++it) {
+            const uint32_t acc = it & 1u;
+            if (elected) go_flag = mbar_wait<kPair>(&tfull[acc], (it >> 1) & 1u, &abort_flag, a.status, true);
+            named_bar_sync(1, kLinEpi);
+            if (!go_flag) break;
+            tc_fence_after();
+            int r, j;
+            lin_tile(p, tile, r, j);
+            const int n = (kPair ? r * 256 + (int)rank * 128 : r * 128) + row;
+            const int t0 = j * p.Nt, cols = min(p.Nt, a.T - t0);
+            const float bias = a.bias && n < a.N ? bf16_bits_to_f32(__ldg(a.bias + n)) : 0.f;
+            const uint32_t tbase = tmem_base + acc * kLinAccStride + ((uint32_t)(q * 32) << 16);
+            if (k1 - k0 == p.nk) {
+                for (int c0 = half * 32; c0 < cols; c0 += 64) {
+                    float v[32];
+                    tmem_ld32(tbase + (uint32_t)c0, v);
+                    if (n < a.N) lin_store32(a, t0 + c0, cols - c0, n, bias, v);
+                }
+                tc_fence_before();
+                named_bar_sync(1, kLinEpi);
+                if (elected) release(acc);
+                continue;
+            }
+            // a share of the tile: its sums to the workspace, [column / 4][128 rows] float4
+            const long long s0 = (long long)(tile - workers * p.waves) * p.nk, total = (long long)p.rest * p.nk;
+            const int first = (int)(((s0 + 1) * p.sharers - 1) / total);
+            const int last = (int)(((s0 + p.nk) * p.sharers - 1) / total);
+            auto part = [&](int w) {
+                const int slot = ((w * 2 + (w == first)) << kPair) + (int)rank;
+                return reinterpret_cast<float4 *>(a.scratch + (size_t)slot * 128 * p.Nt) + row;
+            };
+            float4 *mine = part(worker);
+            for (int c0 = half * 32; c0 < p.Nt; c0 += 64) {
+                float v[32];
+                tmem_ld32(tbase + (uint32_t)c0, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c0 + 4 * i < p.Nt)
+                        __stcg(mine + (c0 / 4 + i) * 128, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            }
+            tc_fence_before();
+            __threadfence();
+            named_bar_sync(1, kLinEpi);
+            if (elected) {
+                release(acc);
+                int32_t *ctr = a.sync + ((first << kPair) + (int)rank);
+                last_flag = atomicAdd(ctr, 1) == last - first;
+                if (last_flag) *ctr = 0;
+                __threadfence();
+            }
+            named_bar_sync(1, kLinEpi);
+            if (!last_flag) continue;
+            for (int c0 = half * 32; c0 < cols; c0 += 64) {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 2
+                for (int w = first; w <= last; ++w) {
+                    const float4 *src = part(w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c0 + 4 * i < p.Nt) {
+                            const float4 o = __ldcg(src + (c0 / 4 + i) * 128);
+                            v[4 * i] += o.x;
+                            v[4 * i + 1] += o.y;
+                            v[4 * i + 2] += o.z;
+                            v[4 * i + 3] += o.w;
+                        }
+                }
+                if (n < a.N) lin_store32(a, t0 + c0, cols - c0, n, bias, v);
+            }
+        }
+    }
+
+    __syncthreads();
+    if constexpr (kPair) cluster_sync();  // the other CTA is done with the shared TMEM allocation and our barriers
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (kPair)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                         "r"(2 * kLinAccStride)
+                         : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                         "r"(2 * kLinAccStride)
+                         : "memory");
+    }
+}
+
+// Single CTAs up to this many tokens, pairs above.
+constexpr int kLinSingleTokens = 64;
+
+// Token tile: the tokens in as few tiles of at most 256 as hold them, rounded up to 16.
+int lin_token_tile(int T) {
+    const int tiles = (T + 255) / 256;
+    return ((T + tiles - 1) / tiles + 15) / 16 * 16;
+}
+
+template <bool kPair>
+cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
+    constexpr int kSlices = kPair ? 1 : 2;
+    LinPlan p{};
+    p.a = a;
+    p.Nt = lin_token_tile(a.T);
+    p.nk = (a.K + 63) / 64;
+    p.rt = (a.N + (kPair ? 255 : 127)) / (kPair ? 256 : 128);
+    p.tt = (a.T + p.Nt - 1) / p.Nt;
+    const long long tiles = (long long)p.rt * p.tt;
+    if (tiles >= (1ll << 30)) return cudaErrorInvalidValue;
+    int workers = kPair ? sms / 2 : sms;
+    p.waves = (int)(tiles / workers);
+    p.rest = (int)(tiles % workers);
+    // the rest's K slices over the whole grid, unless that shortens it by less than
+    // adding the partials costs
+    p.sharers = p.rest;
+    if (p.rest > 0) {
+        const int split = std::max(1, (int)std::sqrt(kPair ? p.nk / 4 : p.nk));
+        const int s = std::min(workers, p.rest * std::min(split, std::max(1, p.nk / 4)));
+        if ((long long)(s - p.rest) * p.nk >= 6ll * s) p.sharers = s;
+    }
+    if (p.waves == 0) workers = p.sharers;
+    const int brows = kPair ? p.Nt / 2 : p.Nt;
+    const int stage = kSlices * (kLinSliceA + (brows * 128 + 1023) / 1024 * 1024);
+    p.stages = std::min(kLinMaxStages, kLinRing / stage);
+    LinMaps m;
+    if (!encode_2d(&m.w, a.w, a.N, a.K, 128) || !encode_2d(&m.x, a.x, a.T, a.K, brows)) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + (size_t)p.stages * stage;
+    static std::atomic<int> attr_set[64];  // per device: opted in to the ring's shared memory
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(linear_kernel<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kLinRing);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kPair ? 2 * workers : workers);
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kPair ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, linear_kernel<kPair>, m, p);
 }
 
 }  // namespace
 
-size_t linear_scratch_bytes(int, int, int) { return 0; }
+size_t linear_scratch_bytes(int T, int N, int K) {
+    (void)N;
+    (void)K;
+    return T == 0 ? 0 : (size_t)kLinMaxSms * 2 * 128 * lin_token_tile(T) * 4;  // two partials per CTA
+}
 
 cudaError_t launch_linear(const LinearArgs &a, cudaStream_t st) {
-    const dim3 grid((a.N + kTile - 1) / kTile, (a.T + kTile - 1) / kTile);
-    linear_kernel<<<grid, 256, 0, st>>>(a);
-    return cudaGetLastError();
+    const int sms = std::min(device_sm_count(), kLinMaxSms);
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    return a.T <= kLinSingleTokens || sms < 2 ? launch_shape<false>(a, sms, st) : launch_shape<true>(a, sms, st);
 }
 
 }  // namespace moe

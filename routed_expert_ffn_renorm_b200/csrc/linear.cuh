@@ -1,4 +1,4 @@
-// Argument block, epilogue and launch of the fused linear map (linear.cu).
+// Argument block, activations and launch of the fused linear map (linear.cu).
 #pragma once
 
 #include "moe_internal.cuh"
@@ -16,23 +16,12 @@ struct LinearArgs {
     float *scratch;
 };
 
-__device__ __forceinline__ float linear_act(float v, int act) {
-    if (act == MOE_ACT_RELU) return v < 0.f ? 0.f : v;  // a NaN stays
-    if (act == MOE_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678118654752f);  // no cancellation for v < 0
-    if (act == MOE_ACT_SILU) return v / (1.f + expf(-v));
+template <int kAct>
+__device__ __forceinline__ float linear_act(float v) {
+    if (kAct == MOE_ACT_RELU) return v < 0.f ? 0.f : v;  // a NaN stays
+    if (kAct == MOE_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678118654752f);  // no cancellation for v < 0
+    if (kAct == MOE_ACT_SILU) return v / (1.f + expf(-v));
     return v;
-}
-
-// The epilogue of one output: everything in fp32, rounded once.
-__device__ __forceinline__ void linear_store(const LinearArgs &a, int t, int n, float v) {
-    if (a.bias) v += bf16_bits_to_f32(__ldg(a.bias + n));
-    v = linear_act(v, a.act);
-    const size_t o = (size_t)t * a.N + n;
-    if (a.residual) v += bf16_bits_to_f32(a.residual[o]);
-    if (a.out_f32)
-        static_cast<float *>(a.out)[o] = v;
-    else
-        static_cast<uint16_t *>(a.out)[o] = f32_to_bf16_bits(v);
 }
 
 size_t linear_scratch_bytes(int T, int N, int K);
