@@ -18,14 +18,16 @@
 // Tiles go to the grid in whole waves, in bands of 8 row tiles so that a wave's
 // operands stay in L2; the tiles that would make up a last, partial wave have
 // their K range cut into equal contiguous shares over the whole grid.  Shares of
-// a tile leave fp32 partials in the workspace, and the last CTA to arrive adds
-// them in share order: the same bits on every run, and nobody waits.
+// a tile leave fp32 partials in the workspace, and the last warp to arrive at a
+// 32 x 32 block adds them in share order: the same bits on every run, and nobody
+// waits.
 //
-// Roles: warp 0 TMA producer (one lane), warp 1 TMEM allocation and MMA issue
-// (one lane), warps 2..9 epilogue (two to each TMEM lane quarter, on alternate
-// 32-column blocks).  A lane holds one output channel, so a warp's store of one
-// token covers 32 consecutive channels.  Every wait is bounded: past the limit
-// the kernel sets MOE_STATUS_TIMEOUT and every role stops.
+// Roles: warps 0 and 1 TMA producers of W and of the tokens (one lane each),
+// warp 2 TMEM allocation and MMA issue (one lane), warps 3..10 epilogue (two to
+// each TMEM lane quarter, on alternate 32-column blocks).  A lane holds one
+// output channel, so a warp's store of one token covers 32 consecutive
+// channels.  Every wait is bounded: past the limit the kernel sets
+// MOE_STATUS_TIMEOUT and every role stops.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -38,14 +40,15 @@ namespace moe {
 namespace {
 using namespace tc;
 
-constexpr int kLinThreads = 320;
-constexpr int kLinEpi = 256;
+constexpr int kLinEpi = 256;                   // epilogue threads
+constexpr int kLinThreads = 96 + kLinEpi;
 constexpr int kLinMaxSms = 160;                // no device has more SMs (workspace sizing)
 constexpr int kLinSliceA = 128 * 128;          // 128 rows of W x 64 columns
 constexpr int kLinRing = 216 * 1024;           // at most
 constexpr int kLinAccStride = 256;             // TMEM columns between the two accumulators
 constexpr int kLinBand = 8;                    // row tiles of a band
 constexpr int kLinMaxStages = 16;
+constexpr int kLinMaxSplit = 12;               // shares of a tile: at most 14 (unaligned ends), counted in 4 bits
 
 struct __align__(64) LinMaps {
     CUtensorMap w;  // [N, K], box 64 x 128
@@ -98,17 +101,40 @@ __device__ __forceinline__ void lin_tile(const LinPlan &p, int tile, int &r, int
     r = band * kLinBand + in - j * rows;
 }
 
-// Channel n of tokens t0 .. t0 + count - 1 from the sums v: everything in fp32, rounded once.
-__device__ __forceinline__ void lin_store32(const LinearArgs &a, int t0, int count, int n, float bias, float (&v)[32]) {
-    const size_t o = (size_t)t0 * a.N + n;
-    float res[32];
+// The residual of channel n (clamped to the last) and 32 tokens from t0 (behind
+// the last: the last's).  Without a condition on the loads: 32 conditional ones
+// ran one after the other, 14 us a block instead of 1.
+__device__ __forceinline__ void lin_residual(const LinearArgs &a, int t0, int n, uint32_t (&res)[32]) {
+    if (!a.residual) return;
+    const uint16_t *src = a.residual + min(n, a.N - 1);
+    if (t0 + 32 <= a.T) {
+        src += (size_t)t0 * a.N;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) res[i] = 0.f;
-    if (a.residual) {  // all read before the first store: out may be the residual
+        for (int i = 0; i < 32; ++i) res[i] = src[(size_t)i * a.N];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) res[i] = src[(size_t)min(t0 + i, a.T - 1) * a.N];
+    }
+}
+
+// Channel n of `count` tokens from t0: the epilogue of the sums v, in fp32, rounded once.
+template <bool kFull>
+__device__ __forceinline__ void lin_store32(const LinearArgs &a, int t0, int count, int n, const float (&v)[32]) {
+    const size_t o = (size_t)t0 * a.N + n, ld = a.N;
+    if (a.out_f32) {
+        float *out = static_cast<float *>(a.out) + o;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (i < count) res[i] = bf16_bits_to_f32(a.residual[o + (size_t)i * a.N]);
+            if (kFull || i < count) out[i * ld] = v[i];
+    } else {
+        uint16_t *out = static_cast<uint16_t *>(a.out) + o;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (kFull || i < count) out[i * ld] = f32_to_bf16_bits(v[i]);
     }
+}
+__device__ __forceinline__ void lin_epilogue(const LinearArgs &a, int t0, int count, int n, float bias,
+                                             const uint32_t (&res)[32], float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] += bias;
     if (a.act == MOE_ACT_RELU) {
@@ -121,17 +147,13 @@ __device__ __forceinline__ void lin_store32(const LinearArgs &a, int t0, int cou
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_SILU>(v[i]);
     }
-    if (a.out_f32) {
-        float *out = static_cast<float *>(a.out) + o;
+    if (a.residual) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < count) out[(size_t)i * a.N] = v[i] + res[i];
-    } else {
-        uint16_t *out = static_cast<uint16_t *>(a.out) + o;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < count) out[(size_t)i * a.N] = f32_to_bf16_bits(v[i] + res[i]);
+        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(res[i] << 16);
     }
+    if (n >= a.N) return;
+    if (count >= 32) lin_store32<true>(a, t0, 32, n, v);
+    else lin_store32<false>(a, t0, count, n, v);
 }
 
 template <bool kPair>
@@ -142,7 +164,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[kLinMaxStages], empty[kLinMaxStages], tfull[2], tempty[2], mma_done;
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile int abort_flag, go_flag, last_flag;
+    __shared__ volatile int abort_flag, go_flag;
     const LinearArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = kPair ? cluster_ctarank() : 0u;
@@ -150,12 +172,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int workers = kPair ? (int)gridDim.x >> 1 : (int)gridDim.x;
     const uint32_t brows = kPair ? (uint32_t)p.Nt >> 1 : (uint32_t)p.Nt;  // token rows this CTA loads
     const uint32_t slice = kLinSliceA + (brows * 128 + 1023) / 1024 * 1024;
-    const uint32_t slice_tx = kLinSliceA + brows * 128;
     pdl_launch_dependents();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 2);  // the two producers
             mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -171,7 +192,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         prefetch_tmap(&maps.w);
         prefetch_tmap(&maps.x);
     }
-    if (warp == 1) {
+    if (warp == 2) {
         if constexpr (kPair) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
                          "r"(2 * kLinAccStride)
@@ -192,12 +213,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     pdl_wait();  // the operands and the workspace are ready past this point
 
     int tile, k0, k1;
-    if (warp == 0) {
-        // ================= TMA producer =================
+    if (warp < 2) {
+        // ================= TMA producers: W (warp 0) and tokens (warp 1) =================
+        // A copy costs its issuing thread about 75 ns, a slice of a full pair's tile
+        // 240 ns of MMA: one thread for both operands and the barriers held the pair at 60%.
         if (lane == 0) {
-            // few tokens: every weight is read once.  Otherwise the bands' repeats hit L2
-            const uint64_t wpol = p.tt == 1 ? policy_evict_first() : policy_evict_normal();
-            const uint64_t xpol = policy_evict_normal();
+            const CUtensorMap *map = warp == 0 ? &maps.w : &maps.x;
+            const uint32_t off = warp == 0 ? 0u : (uint32_t)kLinSliceA;
+            const uint32_t tx = warp == 0 ? (uint32_t)kLinSliceA : brows * 128;
+            // a single token tile: every weight is read once.  Otherwise the bands' repeats hit L2
+            const uint64_t pol = warp == 0 && p.tt == 1 ? policy_evict_first() : policy_evict_normal();
             LinWalk walk(p, worker, workers);
             uint32_t issued = 0, ph = 0;
             int st = 0;
@@ -205,8 +230,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             while (ok && walk.next(tile, k0, k1)) {
                 int r, j;
                 lin_tile(p, tile, r, j);
-                const int wrow = kPair ? r * 256 + (int)rank * 128 : r * 128;
-                const int xrow = j * p.Nt + (int)(rank * brows);
+                const int y = warp == 0 ? (kPair ? r * 256 + (int)rank * 128 : r * 128) : j * p.Nt + (int)(rank * brows);
                 for (int k = k0; k < k1; k += kSlices) {
                     const int n = min(kSlices, k1 - k);
                     if (issued >= (uint32_t)p.stages &&
@@ -214,18 +238,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         ok = false;
                         break;
                     }
-                    uint8_t *dst = ring + (size_t)st * kSlices * slice;
+                    uint8_t *dst = ring + (size_t)st * kSlices * slice + off;
                     if constexpr (kPair) {  // both CTAs' copies complete on CTA 0's barrier
-                        if (rank == 0) mbar_arrive_expect_tx(&full[st], 2u * slice_tx);
-                        const uint32_t bar0 = mapa(smem_u32(&full[st]), 0);
-                        tma_load_2d_pair(&maps.w, bar0, dst, k * 64, wrow, wpol);
-                        tma_load_2d_pair(&maps.x, bar0, dst + kLinSliceA, k * 64, xrow, xpol);
+                        if (rank == 0) mbar_arrive_expect_tx(&full[st], 2u * tx);
+                        tma_load_2d_pair(map, mapa(smem_u32(&full[st]), 0), dst, k * 64, y, pol);
                     } else {
-                        mbar_arrive_expect_tx(&full[st], (uint32_t)n * slice_tx);
-                        for (int u = 0; u < n; ++u) {
-                            tma_load_2d_hint(&maps.w, &full[st], dst + u * slice, (k + u) * 64, wrow, wpol);
-                            tma_load_2d(&maps.x, &full[st], dst + u * slice + kLinSliceA, (k + u) * 64, xrow);
-                        }
+                        mbar_arrive_expect_tx(&full[st], (uint32_t)n * tx);
+                        for (int u = 0; u < n; ++u)
+                            tma_load_2d_hint(map, &full[st], dst + u * slice, (k + u) * 64, y, pol);
                     }
                     ++issued;
                     if (++st == p.stages) {
@@ -242,7 +262,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     mbar_wait(&full[n % p.stages], (n / p.stages) & 1u, &abort_flag, a.status, false);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 2) {
         // ================= MMA issuer =================
         if (lane == 0 && rank == 0) {
             const uint32_t idesc = idesc_bf16(p.Nt, kPair ? 256 : 128);
@@ -291,8 +311,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
     } else {
         // ================= epilogue =================
-        const int q = warp & 3, half = (warp - 2) >> 2, row = q * 32 + lane;
-        const bool elected = threadIdx.x == 64;
+        const int q = warp & 3, half = (warp - 3) >> 2, row = q * 32 + lane;
+        const bool elected = threadIdx.x == 96;
         auto release = [&](uint32_t acc) {
             if (kPair && rank != 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
             else mbar_arrive(&tempty[acc]);
@@ -300,21 +320,28 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         LinWalk walk(p, worker, workers);
         for (uint32_t it = 0; walk.next(tile, k0, k1); ++it) {
             const uint32_t acc = it & 1u;
-            if (elected) go_flag = mbar_wait<kPair>(&tfull[acc], (it >> 1) & 1u, &abort_flag, a.status, true);
-            named_bar_sync(1, kLinEpi);
-            if (!go_flag) break;
-            tc_fence_after();
             int r, j;
             lin_tile(p, tile, r, j);
             const int n = (kPair ? r * 256 + (int)rank * 128 : r * 128) + row;
             const int t0 = j * p.Nt, cols = min(p.Nt, a.T - t0);
+            const bool whole = k1 - k0 == p.nk;
+            uint32_t next[32];  // the coming block's residual, read ahead of its sums
+            if (whole && half * 32 < cols) lin_residual(a, t0 + half * 32, n, next);
+            if (elected) go_flag = mbar_wait<kPair>(&tfull[acc], (it >> 1) & 1u, &abort_flag, a.status, true);
+            named_bar_sync(1, kLinEpi);
+            if (!go_flag) break;
+            tc_fence_after();
             const float bias = a.bias && n < a.N ? bf16_bits_to_f32(__ldg(a.bias + n)) : 0.f;
             const uint32_t tbase = tmem_base + acc * kLinAccStride + ((uint32_t)(q * 32) << 16);
-            if (k1 - k0 == p.nk) {
+            if (whole) {
                 for (int c0 = half * 32; c0 < cols; c0 += 64) {
+                    uint32_t res[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) res[i] = next[i];
+                    if (c0 + 64 < cols) lin_residual(a, t0 + c0 + 64, n, next);
                     float v[32];
                     tmem_ld32(tbase + (uint32_t)c0, v);
-                    if (n < a.N) lin_store32(a, t0 + c0, cols - c0, n, bias, v);
+                    lin_epilogue(a, t0 + c0, cols - c0, n, bias, res, v);
                 }
                 tc_fence_before();
                 named_bar_sync(1, kLinEpi);
@@ -325,56 +352,62 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const long long s0 = (long long)(tile - workers * p.waves) * p.nk, total = (long long)p.rest * p.nk;
             const int first = (int)(((s0 + 1) * p.sharers - 1) / total);
             const int last = (int)(((s0 + p.nk) * p.sharers - 1) / total);
+            const int blocks = (p.Nt + 31) / 32;
             auto part = [&](int w) {
                 const int slot = ((w * 2 + (w == first)) << kPair) + (int)rank;
-                return reinterpret_cast<float4 *>(a.scratch + (size_t)slot * 128 * p.Nt) + row;
+                return reinterpret_cast<float4 *>(a.scratch + (size_t)slot * 128 * 32 * blocks) + row;
             };
-            float4 *mine = part(worker);
+            // Every warp settles its 32 x 32 blocks by itself: all sums out, then block
+            // by block a count, and whoever counts last adds the block up.  The shares
+            // start at different blocks, so that the adding falls to all of them.
+            const int nb = (blocks - half + 1) / 2;
             for (int c0 = half * 32; c0 < p.Nt; c0 += 64) {
                 float v[32];
                 tmem_ld32(tbase + (uint32_t)c0, v);
+                float4 *dst = part(worker) + c0 / 4 * 128;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (c0 + 4 * i < p.Nt)
-                        __stcg(mine + (c0 / 4 + i) * 128, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                for (int c = 0; c < 8; ++c)
+                    __stcg(dst + c * 128, make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
             }
             tc_fence_before();
             __threadfence();
             named_bar_sync(1, kLinEpi);
-            if (elected) {
-                release(acc);
-                int32_t *ctr = a.sync + ((first << kPair) + (int)rank);
-                last_flag = atomicAdd(ctr, 1) == last - first;
-                if (last_flag) *ctr = 0;
-                __threadfence();
-            }
-            named_bar_sync(1, kLinEpi);
-            if (!last_flag) continue;
-            for (int c0 = half * 32; c0 < cols; c0 += 64) {
+            if (elected) release(acc);
+            uint32_t *ctr = reinterpret_cast<uint32_t *>(a.sync) + ((first << kPair) + (int)rank) * 4 + q;
+            for (int i = 0, at = nb * (worker - first) / (last - first + 1); i < nb; ++i, at = at + 1 < nb ? at + 1 : 0) {
+                const int blk = 2 * at + half, c0 = 32 * blk;
+                int is_last = 0;
+                if (lane == 0) {
+                    const uint32_t one = 1u << (4 * blk), shares = (uint32_t)(last - first + 1);
+                    is_last = (atomicAdd(ctr, one) >> (4 * blk) & 15u) == shares - 1u;
+                    if (is_last) atomicSub(ctr, shares * one);
+                    __threadfence();
+                }
+                if (!__shfl_sync(0xffffffffu, is_last, 0)) continue;
                 float v[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                for (int c = 0; c < 32; ++c) v[c] = 0.f;
+                if (c0 < cols) lin_residual(a, t0 + c0, n, next);
 #pragma unroll 2
                 for (int w = first; w <= last; ++w) {
-                    const float4 *src = part(w);
+                    const float4 *src = part(w) + c0 / 4 * 128;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c0 + 4 * i < p.Nt) {
-                            const float4 o = __ldcg(src + (c0 / 4 + i) * 128);
-                            v[4 * i] += o.x;
-                            v[4 * i + 1] += o.y;
-                            v[4 * i + 2] += o.z;
-                            v[4 * i + 3] += o.w;
-                        }
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 o = __ldcg(src + c * 128);
+                        v[4 * c] += o.x;
+                        v[4 * c + 1] += o.y;
+                        v[4 * c + 2] += o.z;
+                        v[4 * c + 3] += o.w;
+                    }
                 }
-                if (n < a.N) lin_store32(a, t0 + c0, cols - c0, n, bias, v);
+                if (c0 < cols) lin_epilogue(a, t0 + c0, cols - c0, n, bias, next, v);
             }
         }
     }
 
     __syncthreads();
     if constexpr (kPair) cluster_sync();  // the other CTA is done with the shared TMEM allocation and our barriers
-    if (warp == 1) {
+    if (warp == 2) {
         tc_fence_after();
         if constexpr (kPair)
             asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
@@ -414,9 +447,9 @@ cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
     // adding the partials costs
     p.sharers = p.rest;
     if (p.rest > 0) {
-        const int split = std::max(1, (int)std::sqrt(kPair ? p.nk / 4 : p.nk));
+        const int split = std::min(kLinMaxSplit, std::max(1, (int)std::sqrt(p.nk)));
         const int s = std::min(workers, p.rest * std::min(split, std::max(1, p.nk / 4)));
-        if ((long long)(s - p.rest) * p.nk >= 6ll * s) p.sharers = s;
+        if ((long long)(s - p.rest) * p.nk >= (12ll + p.Nt / 8) * s) p.sharers = s;
     }
     if (p.waves == 0) workers = p.sharers;
     const int brows = kPair ? p.Nt / 2 : p.Nt;
@@ -456,7 +489,7 @@ cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
 size_t linear_scratch_bytes(int T, int N, int K) {
     (void)N;
     (void)K;
-    return T == 0 ? 0 : (size_t)kLinMaxSms * 2 * 128 * lin_token_tile(T) * 4;  // two partials per CTA
+    return T == 0 ? 0 : (size_t)kLinMaxSms * 2 * 128 * ((lin_token_tile(T) + 31) / 32 * 32) * 4;  // two partials per CTA
 }
 
 cudaError_t launch_linear(const LinearArgs &a, cudaStream_t st) {

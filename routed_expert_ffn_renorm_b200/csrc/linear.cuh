@@ -24,6 +24,8 @@ __device__ __forceinline__ float linear_act(float v) {
     return v;
 }
 
+// Ints of the workspace head the kernel counts in (zero between launches).
+constexpr int kLinSyncInts = 4 * 160;
 size_t linear_scratch_bytes(int T, int N, int K);
 cudaError_t launch_linear(const LinearArgs &a, cudaStream_t st);
 

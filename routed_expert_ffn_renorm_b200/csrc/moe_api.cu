@@ -2,6 +2,7 @@
 // sequence.  No entry point allocates, frees or synchronises (except
 // moe_status_read, which waits for its own copy); every launch goes on the
 // caller's stream.
+#include <algorithm>
 #include <cstring>
 #include <mutex>
 
@@ -21,7 +22,7 @@ constexpr size_t kHeadBytes = 8192;
 constexpr size_t kHdoneOffset = 256;
 constexpr size_t kSyncOffset = 4608;
 static_assert(kHdoneOffset + 4 * (kMaxExperts + 2) <= kSyncOffset, "workspace head");
-static_assert(kSyncOffset + 4 * kFewSyncInts <= kHeadBytes, "workspace head");
+static_assert(kSyncOffset + 4 * std::max(kFewSyncInts, kLinSyncInts) <= kHeadBytes, "workspace head");
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct WsLayout {
