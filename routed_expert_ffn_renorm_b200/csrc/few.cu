@@ -46,8 +46,8 @@ namespace moe {
 namespace {
 using namespace tc;
 
-constexpr int kFewGroups = 2;                    // consumer groups: each takes its share of a chunk's K steps
-constexpr int kFewConsumers = kFewGroups * 256;  // 8 warps of 16 weight rows per group
+constexpr int kFewGroups = 4;                    // consumer groups: each takes a quarter of a step's columns
+constexpr int kFewConsumers = kFewGroups * 128;  // 4 warps of 32 weight rows per group
 constexpr int kFewThreads = kFewConsumers + 64;  // + weight producer, token producer
 constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;
 constexpr int kFewMaxSms = 160;
@@ -200,23 +200,30 @@ __device__ __forceinline__ float few_weight(const FewArgs &a, const FewRouting &
 
 
 // ------------------------------------------------------------- the stream --
-// Shapes of a ring slot: 128 weight rows of kK columns, their block scales,
-// and up to 2 Tp token rows of kK bf16.
+// A step is two chunks of the K axis (one at the end of an odd count): 128
+// weight rows of 2 kK columns, their block scales, and the same columns of up to
+// 2 Tp token rows.  A ring slot holds one step:
+//   weights [half][chunk][64 rows][kRowBytes] (halves: gate and up, or the two
+//   64-row halves of the down projection), scales [half][chunk][64][per],
+//   tokens [64-column box][rows][128 bytes].
 template <int FMT, int NT>
 struct FewShape {
     static constexpr int kTp = 8 * NT;               // token rows (T rounded up)
     static constexpr int kK = FMT == 0 ? 64 : 128;   // K columns per chunk
     static constexpr int kRowBytes = FMT == 2 ? 64 : 128;
-    static constexpr int kWBytes = 128 * kRowBytes;
-    static constexpr int kScaleBytes = FMT == 0 ? 0 : FMT == 1 ? 512 : 1024;
-    static constexpr int kBoxes = kK / 64;           // 64-column token boxes
-    static constexpr int kXBytes = kBoxes * kTp * 128;
-    static constexpr int kTokOff = kWBytes + 1024 * (FMT != 0);
+    static constexpr int kChunkBytes = 64 * kRowBytes;
+    static constexpr int kWBytes = 4 * kChunkBytes;
+    static constexpr int kRun = FMT == 0 ? 0 : FMT == 1 ? 256 : 512;  // block scales of 64 rows and one chunk
+    static constexpr int kScaleBytes = 4 * kRun;
+    static constexpr int kBoxes = kK / 64;           // 64-column token boxes per chunk
+    static constexpr int kXBytes = 2 * kBoxes * kTp * 128;
+    static constexpr int kTokOff = kWBytes + (kScaleBytes + 1023) / 1024 * 1024;
     static constexpr int kSlotBytes = kTokOff + 2 * kXBytes;
-    static constexpr int kPartFloats = 256 * NT * 4;  // one row block's sums: 8 warps x 32 lanes
-    static constexpr int kFixed = 1024 + (int)sizeof(FewRouting) + kPartFloats * 4 * 2 + 1024;
+    static constexpr int kPartFloats = 256 * NT * 4;  // one row block's sums: 8 tiles of 16 rows x 32 lanes
+    static constexpr int kXchFloats = kFewGroups * kPartFloats > 16 * 128 ? kFewGroups * kPartFloats : 16 * 128;
+    static constexpr int kFixed = 1024 + (int)sizeof(FewRouting) + kXchFloats * 4 + 1024;
     static constexpr int kSlots = (kFewSmem - kFixed) / kSlotBytes;
-    static constexpr int kSmem = 1024 + kSlots * kSlotBytes + kPartFloats * 4 * 2 + (int)sizeof(FewRouting) + 1024;
+    static constexpr int kSmem = kFixed + kSlots * kSlotBytes;
 };
 
 struct __align__(64) FewMaps {
@@ -231,7 +238,7 @@ struct FewPlan {
     int32_t *sync; // [0], [1] grid barriers, [2] CTAs done, [16 + phase * kFewMaxSms + cta] partial arrivals
 };
 
-// This CTA's share of a phase: chunks [lo, hi) of `total`, `per` to a row block.
+// This CTA's share of a phase: steps [lo, hi) of `total`, `per` to a row block.
 struct Share {
     int per, total, ctas, lo, hi;
     __device__ Share(int units, int per_unit) : per(per_unit), total(units * per_unit) {
@@ -242,7 +249,7 @@ struct Share {
             hi = (int)((long long)(blockIdx.x + 1) * total / ctas);
         }
     }
-    // the CTA whose share holds chunk c
+    // the CTA whose share holds step c
     __device__ int owner(int c) const { return (int)(((long long)(c + 1) * ctas - 1) / total); }
 };
 
@@ -280,6 +287,12 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(d) : "r"(a), "r"(sel));
+    return d;
+}
+
 // Sixteen codes of one row as bf16 pairs times their block's scale, exactly.
 //
 // E4M3: the code's sign, exponent and mantissa moved to a bf16's fields are
@@ -294,8 +307,8 @@ __device__ __forceinline__ void decode16_mx(uint32_t (&v)[8], const uint32_t (&c
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t x = __byte_perm(c[j], 0, i ? 0x3424 : 0x1404);  // bytes to the high halves
-                v[2 * j + i] = mul_bf16x2(((x >> 4) & 0x07F007F0u) | (x & 0x80008000u), f);
+                const uint32_t x = prmt(c[j], i ? 0xB3A2u : 0x9180u);  // a code and its sign, eight times, in each half
+                v[2 * j + i] = mul_bf16x2((x << 4) & 0x87F087F0u, f);
             }
     } else {
 #pragma unroll
@@ -323,6 +336,92 @@ __device__ __forceinline__ void decode16_nv(uint32_t (&v)[8], const uint32_t (&c
         }
 }
 
+// One warp's share of a step: 32 weight rows (tiles 2 rg and 2 rg + 1) times a
+// half of chunk `sub`, 32 columns in bf16 and 64 block-scaled ones.  kDown: the
+// tiles are 16 consecutive rows and the token operand is h and its remainder;
+// otherwise a tile is 8 gate rows and the 8 up rows of the same channels.
+template <int FMT, int NT, bool kDown>
+__device__ __forceinline__ void few_step(float (&acc)[2][NT][4], uint32_t slot, int rg, int sub, int half, int lane) {
+    using S = FewShape<FMT, NT>;
+    constexpr int kParts = kDown ? 2 : 1, kBoxBytes = kParts * S::kTp * 128;
+    const int g = lane >> 2, q = lane & 3;
+    const uint32_t tb = slot + S::kTokOff;
+    // the tile's rows 0..7 and 8..15: a half of the step's 128 rows, and a row of it
+    auto row = [&](int m, int hi, int &h) -> uint32_t {
+        const int tile = rg * 2 + m, rr = kDown ? tile * 16 + hi * 8 : hi * 64 + tile * 8;
+        h = rr >> 6;
+        return (uint32_t)(rr & 63);
+    };
+    if constexpr (FMT == 0) {
+        const int mi = lane >> 3, lr = lane & 7;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int ks = half * 2 + s;  // of the chunk's four K16 steps
+            uint32_t A[2][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                int h;
+                const uint32_t rr = row(m, mi & 1, h) + lr;
+                ldsm4(A[m], slot + (h * 2 + sub) * S::kChunkBytes + rr * 128 + (((2 * ks + (mi >> 1)) ^ lr) << 4));
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                uint32_t B[4];  // matrices 0, 1: x or h; 2, 3: the remainder
+                const uint32_t tr = n * 8 + lr + (kDown && mi >= 2 ? S::kTp : 0);
+                ldsm4(B, tb + sub * kBoxBytes + tr * 128 + (((2 * ks + (mi & 1)) ^ lr) << 4));
+#pragma unroll
+                for (int m = 0; m < 2; ++m) mma16816(acc[m][n], A[m][0], A[m][1], A[m][2], A[m][3], B[0], B[1]);
+                if constexpr (kDown) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) mma16816(acc[m][n], A[m][0], A[m][1], A[m][2], A[m][3], B[2], B[3]);
+                }
+            }
+        }
+    } else {
+        // lane (g, q) takes 16 codes of rows g and g + 8 of each tile (one block scale
+        // each) and the same 16 token columns
+        uint32_t v[2][2][8];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                int h;
+                const uint32_t rr = row(m, hi, h) + g;
+                const uint32_t wb = slot + (h * 2 + sub) * S::kChunkBytes, sc = slot + S::kWBytes + (h * 2 + sub) * S::kRun;
+                if constexpr (FMT == 1) {
+                    uint32_t c[4];
+                    lds128(c, wb + rr * 128 + (((half * 4 + q) ^ (rr & 7)) << 4));
+                    decode16_mx(v[m][hi], c, lds8(sc + rr * 4 + half * 2 + (q >> 1)));
+                } else {
+                    uint32_t c[2];
+                    lds64(c, wb + rr * 64 + (((half * 2 + (q >> 1)) ^ ((rr >> 1) & 3)) << 4) + (q & 1) * 8);
+                    decode16_nv(v[m][hi], c, lds8(sc + rr * 8 + half * 4 + q));
+                }
+            }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+                const uint32_t tr = tb + (sub * 2 + half) * kBoxBytes + (part * S::kTp + n * 8 + g) * 128;
+                uint32_t b[8];
+                lds128(reinterpret_cast<uint32_t(&)[4]>(b[0]), tr + (((2 * q) ^ g) << 4));
+                lds128(reinterpret_cast<uint32_t(&)[4]>(b[4]), tr + (((2 * q + 1) ^ g) << 4));
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    uint32_t b0 = b[2 * s], b1 = b[2 * s + 1];
+                    if constexpr (FMT == 2) {  // the columns in the codes' pair order
+                        const uint32_t lo = b[(s >> 1) * 4 + (s & 1)], hi = b[(s >> 1) * 4 + (s & 1) + 2];
+                        b0 = __byte_perm(lo, hi, 0x5410);
+                        b1 = __byte_perm(lo, hi, 0x7632);
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                        mma16816(acc[m][n], v[m][0][2 * s], v[m][1][2 * s], v[m][0][2 * s + 1], v[m][1][2 * s + 1], b0, b1);
+                }
+            }
+    }
+}
+
 template <int FMT, int NT>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewMaps maps, const FewPlan p) {
     using S = FewShape<FMT, NT>;
@@ -330,7 +429,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *xch = reinterpret_cast<float *>(ring + (size_t)kSlots * S::kSlotBytes);  // group 1's sums; projection sums
-    FewRouting &r = *reinterpret_cast<FewRouting *>(xch + 2 * S::kPartFloats);
+    FewRouting &r = *reinterpret_cast<FewRouting *>(xch + S::kXchFloats);
     uint64_t *fullw = reinterpret_cast<uint64_t *>((reinterpret_cast<uintptr_t>(&r + 1) + 7) & ~uintptr_t(7));
     uint64_t *fullb = fullw + kSlots, *empty = fullb + kSlots, *routed = empty + kSlots;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(routed + 1);
@@ -352,65 +451,65 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     __syncthreads();
 
     const int kH = a.H / S::kK, kS = a.Is / S::kK, kI = a.I / S::kK;  // chunks along H, Is, I
+    const int sH = (kH + 1) >> 1, sS = (kS + 1) >> 1, sI = (kI + 1) >> 1;  // steps
     // the three phases' shares; the routed ones are known once the tokens are routed
     auto share = [&](int phase) {
-        return phase == 0 ? Share(a.Is / 64, kH) : phase == 1 ? Share(r.nu * (a.I / 64), kH)
-                                                              : Share(a.H / 128, kS + r.nu * kI);
+        return phase == 0 ? Share(a.Is / 64, sH) : phase == 1 ? Share(r.nu * (a.I / 64), sH)
+                                                              : Share(a.H / 128, sS + r.nu * sI);
     };
 
     if (warp == kFewConsumers / 32) {
         // ================= weight producer =================
         if (lane == 0) {
             const uint64_t pol = policy_evict_first();
-            uint32_t issued = 0;
+            uint32_t st = 0, ph = 0, issued = 0;
             bool ok = true;
+            // one step: chunks kcol .. kcol + n - 1 of rows y0 .. + 63 and y1 .. + 63
+            auto load = [&](const CUtensorMap *m0, const CUtensorMap *m1, const uint8_t *f0, const uint8_t *f1, int y0,
+                            int y1, int kcol, int cols) {
+                if (issued >= (uint32_t)kSlots && !mbar_wait_fast(&empty[st], ph ^ 1u, abort_flag, a.status, true)) {
+                    ok = false;
+                    return;
+                }
+                uint8_t *dst = ring + (size_t)st * S::kSlotBytes;
+                const uint32_t run = S::kRun * (uint32_t)min(2, cols - kcol);
+                mbar_arrive_expect_tx(&fullw[st], S::kWBytes + 2 * run);
+                tma_load_3d_hint(m0, &fullw[st], dst, 0, y0, kcol, pol);
+                tma_load_3d_hint(m1, &fullw[st], dst + S::kWBytes / 2, 0, y1, kcol, pol);
+                if constexpr (FMT != 0) {
+                    bulk_load(dst + S::kWBytes, f0 + ((size_t)(y0 >> 6) * cols + kcol) * S::kRun, run, &fullw[st]);
+                    bulk_load(dst + S::kWBytes + 2 * S::kRun, f1 + ((size_t)(y1 >> 6) * cols + kcol) * S::kRun, run,
+                              &fullw[st]);
+                }
+                ++issued;
+                if (++st == (uint32_t)kSlots) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            };
             for (int phase = 0; ok && phase < 3; ++phase) {
                 if (phase == 1 && !mbar_wait(routed, 0, abort_flag, a.status, true)) break;
                 const Share sh = share(phase);
-                int unit = sh.lo / max(sh.per, 1), kc = sh.lo - unit * sh.per;
-                for (int c = sh.lo; ok && c < sh.hi; ++c) {
-                    const uint32_t st = issued % kSlots, use = issued / kSlots;
-                    if (use > 0 && !mbar_wait_fast(&empty[st], (use - 1) & 1u, abort_flag, a.status, true)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *dst = ring + (size_t)st * S::kSlotBytes;
-                    mbar_arrive_expect_tx(&fullw[st], S::kWBytes + S::kScaleBytes);
-                    const CUtensorMap *m0, *m1;
-                    const uint8_t *f0, *f1;  // packed scales of the two 64-row halves
-                    int x, y0, y1, kcol, cols;
+                int unit = sh.lo / max(sh.per, 1), at = sh.lo - unit * sh.per;
+                for (int left = sh.hi - sh.lo; ok && left > 0; ++unit, at = 0) {
+                    const int end = min(sh.per, at + left);
+                    left -= end - at;
                     if (phase < 2) {
-                        const int per = a.I / 64, e = phase ? r.list[unit / per] : 0;
-                        m0 = phase ? &maps.gate : &maps.s_gate;
-                        m1 = phase ? &maps.up : &maps.s_up;
-                        f0 = phase ? a.gate.sf : a.s_gate.sf;
-                        f1 = phase ? a.up.sf : a.s_up.sf;
-                        kcol = kc;
-                        cols = kH;
-                        y0 = y1 = phase ? e * a.I + unit % per * 64 : unit * 64;
+                        const int per = a.I / 64;
+                        const int y = phase ? r.list[unit / per] * a.I + unit % per * 64 : unit * 64;
+                        const CUtensorMap *m0 = phase ? &maps.gate : &maps.s_gate, *m1 = phase ? &maps.up : &maps.s_up;
+                        const uint8_t *f0 = phase ? a.gate.sf : a.s_gate.sf, *f1 = phase ? a.up.sf : a.s_up.sf;
+                        for (; ok && at < end; ++at) load(m0, m1, f0, f1, y, y, 2 * at, kH);
                     } else {
-                        const bool shared = kc < kS;
-                        const int u = shared ? 0 : (kc - kS) / kI;
-                        m0 = m1 = shared ? &maps.s_down : &maps.down;
-                        f0 = f1 = shared ? a.s_down.sf : a.down.sf;
-                        kcol = shared ? kc : kc - kS - u * kI;
-                        cols = shared ? kS : kI;
-                        y0 = unit * 128 + (shared ? 0 : r.list[u] * a.H);
-                        y1 = y0 + 64;
-                    }
-                    x = kcol * (FMT == 0 ? 64 : S::kRowBytes);
-                    tma_load_2d_hint(m0, &fullw[st], dst, x, y0, pol);
-                    tma_load_2d_hint(m1, &fullw[st], dst + S::kWBytes / 2, x, y1, pol);
-                    if constexpr (FMT != 0) {
-                        constexpr int kRun = S::kScaleBytes / 2;
-                        bulk_load(dst + S::kWBytes, f0 + ((size_t)(y0 / 64) * cols + kcol) * kRun, kRun, &fullw[st]);
-                        bulk_load(dst + S::kWBytes + kRun, f1 + ((size_t)(y1 / 64) * cols + kcol) * kRun, kRun,
-                                  &fullw[st]);
-                    }
-                    ++issued;
-                    if (++kc == sh.per) {
-                        kc = 0;
-                        ++unit;
+                        const int y = unit * 128;
+                        for (; ok && at < min(end, sS); ++at)
+                            load(&maps.s_down, &maps.s_down, a.s_down.sf, a.s_down.sf, y, y + 64, 2 * at, kS);
+                        int u = (at - sS) / sI, in = (at - sS) - u * sI;
+                        for (; ok && at < end; ++u, in = 0) {
+                            const int ye = y + r.list[u] * a.H;
+                            for (; ok && in < sI && at < end; ++in, ++at)
+                                load(&maps.down, &maps.down, a.down.sf, a.down.sf, ye, ye + 64, 2 * in, kI);
+                        }
                     }
                 }
             }
@@ -420,7 +519,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     } else if (warp == kFewConsumers / 32 + 1) {
         // ================= token producer =================
         if (lane == 0) {
-            uint32_t issued = 0;
+            uint32_t st = 0, ph = 0, issued = 0;
             bool ok = true;
             for (int phase = 0; ok && phase < 3; ++phase) {
                 if (phase == 1 && !mbar_wait(routed, 0, abort_flag, a.status, true)) break;
@@ -429,22 +528,28 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                     if (!grid_wait(p.sync + 1, abort_flag, a.status)) break;
                     fence_proxy_async_global();  // h was written by ordinary stores
                 }
-                int kc = sh.lo % max(sh.per, 1);
+                const CUtensorMap *map = phase == 2 ? &maps.h : &maps.x;
+                const uint32_t bytes = phase == 2 ? 2 * S::kXBytes : S::kXBytes;
+                int at = sh.lo % max(sh.per, 1);
                 for (int c = sh.lo; ok && c < sh.hi; ++c) {
-                    const uint32_t st = issued % kSlots, use = issued / kSlots;
-                    if (use > 0 && !mbar_wait_fast(&empty[st], (use - 1) & 1u, abort_flag, a.status, true)) {
+                    if (issued >= (uint32_t)kSlots && !mbar_wait_fast(&empty[st], ph ^ 1u, abort_flag, a.status, true)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *dst = ring + (size_t)st * S::kSlotBytes + S::kTokOff;
-                    const int rows = phase == 2 ? 2 : 1;
-                    mbar_arrive_expect_tx(&fullb[st], rows * S::kXBytes);
-#pragma unroll
-                    for (int b = 0; b < S::kBoxes; ++b)
-                        tma_load_2d(phase == 2 ? &maps.h : &maps.x, &fullb[st], dst + b * rows * kTp * 128,
-                                    kc * S::kK + b * 64, 0);
+                    int chunk = 2 * at;
+                    if (phase == 2 && at >= sS) {  // the routed channels lie behind the shared ones
+                        const int u = (at - sS) / sI;
+                        chunk = kS + u * kI + 2 * (at - sS - u * sI);
+                    }
+                    mbar_arrive_expect_tx(&fullb[st], bytes);
+                    tma_load_3d_hint(map, &fullb[st], ring + (size_t)st * S::kSlotBytes + S::kTokOff, 0, 0,
+                                     chunk * S::kBoxes, policy_evict_normal());
                     ++issued;
-                    if (++kc == sh.per) kc = 0;
+                    if (++st == (uint32_t)kSlots) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                    if (++at == sh.per) at = 0;
                 }
             }
             for (uint32_t n = issued > (uint32_t)kSlots ? issued - kSlots : 0; n < issued; ++n)
@@ -520,30 +625,42 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         few_route(a, r);
         if (tid == 0) mbar_arrive(routed);
 
-        const int grp = warp >> 3, wr = warp & 7, g = lane >> 2, q = lane & 3;
+        const int grp = warp >> 2, rg = warp & 3, g = lane >> 2, q = lane & 3;
+        const int sub = grp >> 1, half = grp & 1;  // this group's columns: a half of a chunk of the step
         bool dead = false;  // a wait gave up: go through the motions to the end
-        uint32_t used = 0;
+        uint32_t st = 0, ph = 0;
         float sg[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) sg[n][0] = sg[n][1] = 0.f;
         for (int phase = 0; phase < 3; ++phase) {
             const Share sh = share(phase);
-            int unit = sh.lo / max(sh.per, 1), kc = sh.lo - unit * sh.per, left = sh.hi - sh.lo;
+            int unit = sh.lo / max(sh.per, 1), at = sh.lo - unit * sh.per, left = sh.hi - sh.lo;
             bool have_sg = false;
             while (left > 0) {
-                const int n_chunks = min(sh.per - kc, left);
-                float acc[NT][4] = {};
+                const int n_steps = min(sh.per - at, left);
+                float acc[2][NT][4] = {};  // two tiles of 16 rows x 8 NT tokens
                 auto scale_shared = [&] {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        acc[n][0] *= sg[n][0];
-                        acc[n][1] *= sg[n][1];
-                        acc[n][2] *= sg[n][0];
-                        acc[n][3] *= sg[n][1];
-                    }
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            acc[m][n][0] *= sg[n][0];
+                            acc[m][n][1] *= sg[n][1];
+                            acc[m][n][2] *= sg[n][0];
+                            acc[m][n][3] *= sg[n][1];
+                        }
                 };
-                for (int i = 0; i < n_chunks; ++i, ++used) {
-                    const uint32_t st = used % kSlots, ph = (used / kSlots) & 1u;
+                // steps until the odd last one of the unit's current K range
+                int in = at, range = phase < 2 ? sH : sS;
+                bool odd = (phase < 2 ? kH : kS) & 1;
+                if (phase == 2 && at >= sS) {
+                    in = (at - sS) % sI;
+                    range = sI;
+                    odd = kI & 1;
+                }
+                for (int i = 0; i < n_steps; ++i) {
+                    // the shared expert's channels come first: their sum takes the gate before the routed ones join
+                    if (phase == 2 && at + i == sS && i > 0) scale_shared();
                     if (!dead) dead = !mbar_wait_fast(&fullw[st], ph, abort_flag, a.status, true);
                     if (!dead) dead = !mbar_wait_fast(&fullb[st], ph, abort_flag, a.status, true);
                     if (phase == 2 && !have_sg) {  // the token operand is past the grid barrier: so are the gates
@@ -556,95 +673,51 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                                 sg[n][c] = a.Is > 0 && t < a.T ? __ldcg(a.sgate + t) : 0.f;
                             }
                     }
-                    // the shared expert's channels come first: their sum takes the gate before the routed ones join
-                    if (phase == 2 && kc + i == kS && i > 0) scale_shared();
-                    const uint32_t wb = smem_u32(ring + (size_t)st * S::kSlotBytes), tb = wb + S::kTokOff;
-                    // rows 0..7 and 8..15 of this warp's tile within the slot
-                    const uint32_t r0 = phase < 2 ? wr * 8 : wr * 16, r1 = phase < 2 ? 64 + wr * 8 : wr * 16 + 8;
-                    if constexpr (FMT == 0) {
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {  // this group's two of the four K16 steps
-                            const int ks = grp * 2 + s, mi = lane >> 3, lr = lane & 7;
-                            uint32_t A[4];
-                            ldsm4(A, wb + ((mi & 1 ? r1 : r0) + lr) * 128 + (((2 * ks + (mi >> 1)) ^ lr) << 4));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                // matrices 0, 1: h (or x), 2, 3: its remainder
-                                uint32_t B[4];
-                                const uint32_t row = n * 8 + lr + (phase == 2 && mi >= 2 ? kTp : 0);
-                                ldsm4(B, tb + row * 128 + (((2 * ks + (mi & 1)) ^ lr) << 4));
-                                mma16816(acc[n], A[0], A[1], A[2], A[3], B[0], B[1]);
-                                if (phase == 2) mma16816(acc[n], A[0], A[1], A[2], A[3], B[2], B[3]);
-                            }
-                        }
-                    } else {
-                        // this group's 64 of the 128 columns: lane (g, q) takes 16 codes of rows
-                        // g and g + 8 (one block scale each) and the same 16 token columns
-                        uint32_t v0[8], v1[8];
-                        const uint32_t ra = r0 + g, rb = r1 + g;
-                        if constexpr (FMT == 1) {
-                            uint32_t c0[4], c1[4];
-                            lds128(c0, wb + ra * 128 + (((grp * 4 + q) ^ (ra & 7)) << 4));
-                            lds128(c1, wb + rb * 128 + (((grp * 4 + q) ^ (rb & 7)) << 4));
-                            const uint32_t sc = wb + S::kWBytes + grp * 2 + (q >> 1);
-                            decode16_mx(v0, c0, lds8(sc + ra * 4));
-                            decode16_mx(v1, c1, lds8(sc + rb * 4));
-                        } else {
-                            uint32_t c0[2], c1[2];
-                            const uint32_t un = grp * 2 + (q >> 1), in = (q & 1) * 8;
-                            lds64(c0, wb + ra * 64 + ((un ^ ((ra >> 1) & 3)) << 4) + in);
-                            lds64(c1, wb + rb * 64 + ((un ^ ((rb >> 1) & 3)) << 4) + in);
-                            const uint32_t sc = wb + S::kWBytes + grp * 4 + q;
-                            decode16_nv(v0, c0, lds8(sc + ra * 8));
-                            decode16_nv(v1, c1, lds8(sc + rb * 8));
-                        }
-                        const int parts = phase == 2 ? 2 : 1;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int part = 0; part < 2; ++part) {
-                                if (part == 1 && phase != 2) break;
-                                const uint32_t row = tb + (uint32_t)(grp * parts * kTp + part * kTp + n * 8 + g) * 128;
-                                uint32_t b[8];
-                                lds128(reinterpret_cast<uint32_t(&)[4]>(b[0]), row + (((2 * q) ^ g) << 4));
-                                lds128(reinterpret_cast<uint32_t(&)[4]>(b[4]), row + (((2 * q + 1) ^ g) << 4));
-#pragma unroll
-                                for (int s = 0; s < 4; ++s) {
-                                    uint32_t b0 = b[2 * s], b1 = b[2 * s + 1];
-                                    if constexpr (FMT == 2) {  // the columns in the codes' pair order
-                                        const uint32_t lo = b[(s >> 1) * 4 + (s & 1)], hi = b[(s >> 1) * 4 + (s & 1) + 2];
-                                        b0 = __byte_perm(lo, hi, 0x5410);
-                                        b1 = __byte_perm(lo, hi, 0x7632);
-                                    }
-                                    mma16816(acc[n], v0[2 * s], v1[2 * s], v0[2 * s + 1], v1[2 * s + 1], b0, b1);
-                                }
-                            }
+                    const bool live = sub == 0 || !(odd && in == range - 1);
+                    if (++in == range) {
+                        in = 0;
+                        range = sI;  // only the down projection goes on to another range
+                        odd = kI & 1;
+                    }
+                    if (live) {
+                        const uint32_t slot = smem_u32(ring + (size_t)st * S::kSlotBytes);
+                        if (phase == 2) few_step<FMT, NT, true>(acc, slot, rg, sub, half, lane);
+                        else few_step<FMT, NT, false>(acc, slot, rg, sub, half, lane);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&empty[st]);
-                }
-                if (phase == 2 && kc < kS && kc + n_chunks <= kS) scale_shared();  // the shared part alone
-                // both groups' sums
-                if (grp == 1) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        *reinterpret_cast<float4 *>(xch + (n * 256 + wr * 32 + lane) * 4) =
-                            make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-                }
-                named_bar_sync(2, kFewConsumers);
-                if (grp == 0) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float4 o = *reinterpret_cast<const float4 *>(xch + (n * 256 + wr * 32 + lane) * 4);
-                        acc[n][0] += o.x;
-                        acc[n][1] += o.y;
-                        acc[n][2] += o.z;
-                        acc[n][3] += o.w;
+                    if (++st == (uint32_t)kSlots) {
+                        st = 0;
+                        ph ^= 1u;
                     }
                 }
+                if (phase == 2 && at < sS && at + n_steps <= sS) scale_shared();  // the shared part alone
+                // the groups' sums
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                        *reinterpret_cast<float4 *>(xch + (((grp * NT + n) * 8 + rg * 2 + m) * 32 + lane) * 4) =
+                            make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+                named_bar_sync(2, kFewConsumers);
+                float sum[NT][4] = {};
+                if (warp < 8) {  // tile `warp` of the row block
+#pragma unroll
+                    for (int k = 0; k < kFewGroups; ++k)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float4 o =
+                                *reinterpret_cast<const float4 *>(xch + (((k * NT + n) * 8 + warp) * 32 + lane) * 4);
+                            sum[n][0] += o.x;
+                            sum[n][1] += o.y;
+                            sum[n][2] += o.z;
+                            sum[n][3] += o.w;
+                        }
+                }
                 named_bar_sync(3, kFewConsumers);
-                if (grp == 0) {
-                    bool whole = n_chunks == sh.per;
+                if (warp < 8) {
+                    const int wr = warp;
+                    bool whole = n_steps == sh.per;
                     if (!whole) {
                         // a row block shared with other CTAs: the last to arrive adds the partials
                         const int first = sh.owner(unit * sh.per), last = sh.owner(unit * sh.per + sh.per - 1);
@@ -655,7 +728,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                         };
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            __stcg(slot(cta) + n * 256, make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]));
+                            __stcg(slot(cta) + n * 256, make_float4(sum[n][0], sum[n][1], sum[n][2], sum[n][3]));
                         __threadfence();
                         named_bar_sync(4, 256);
                         if (tid == 0) {
@@ -669,15 +742,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                         whole = *last_flag != 0;
                         if (whole) {
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+                            for (int n = 0; n < NT; ++n) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0.f;
                             for (int c = first; c <= last; ++c)
 #pragma unroll
                                 for (int n = 0; n < NT; ++n) {
                                     const float4 o = __ldcg(slot(c) + n * 256);
-                                    acc[n][0] += o.x;
-                                    acc[n][1] += o.y;
-                                    acc[n][2] += o.z;
-                                    acc[n][3] += o.w;
+                                    sum[n][0] += o.x;
+                                    sum[n][1] += o.y;
+                                    sum[n][2] += o.z;
+                                    sum[n][3] += o.w;
                                 }
                         }
                     }
@@ -700,8 +773,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                                 const int t = n * 8 + 2 * q + c;
                                 float v = 0.f;
                                 if ((tokens >> t) & 1u) {
-                                    const float gv = acc[n][c] * tg;
-                                    v = gv / (1.f + expf(-gv)) * (acc[n][2 + c] * tu) * td;
+                                    const float gv = sum[n][c] * tg;
+                                    v = gv / (1.f + expf(-gv)) * (sum[n][2 + c] * tu) * td;
                                     if (phase) v *= few_weight(a, r, t, e);
                                 }
                                 const uint16_t hi = f32_to_bf16_bits(v);
@@ -717,15 +790,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
                                 const int t = n * 8 + 2 * q + (c & 1);
-                                if (t < a.T) a.out[(size_t)t * a.H + o + (c >> 1) * 8] = f32_to_bf16_bits(acc[n][c]);
+                                if (t < a.T) a.out[(size_t)t * a.H + o + (c >> 1) * 8] = f32_to_bf16_bits(sum[n][c]);
                             }
                     }
                 }
-                left -= n_chunks;
-                kc = 0;
+                left -= n_steps;
+                at = 0;
                 ++unit;
             }
-            if (phase == 1 && grp == 0) {  // this CTA's part of h is written
+            if (phase == 1 && warp < 8) {  // this CTA's part of h is written
                 fence_proxy_async_global();
                 __threadfence();
                 named_bar_sync(4, 256);
@@ -746,16 +819,16 @@ size_t part_bytes(int tp) { return (size_t)3 * kFewMaxSms * 2 * 128 * tp * 4; }
 int few_ldh(int T, int E, int I, int k, int Is) { return Is + std::min(E, T * k) * I; }
 int few_tp(int T) { return T <= 8 ? 8 : 16; }
 
+// Weights [rows, K] as [K / chunk][rows][chunk bytes]: a box of 64 rows and two chunks.
 template <int FMT>
 bool encode_weights(CUtensorMap *m, const void *base, uint64_t rows, uint64_t K) {
-    if (FMT == 0) return encode_2d(m, base, rows, K, 64);
-    return FMT == 1 ? encode_2d_u8(m, base, rows, K, 64, 128) : encode_2d_u8(m, base, rows, K / 2, 64, 64);
+    return encode_3d(m, base, rows, FMT == 0 ? 2 * K : FMT == 1 ? K : K / 2, FMT == 2 ? 64 : 128, 64, 2);
 }
 
 template <int FMT, int NT>
 cudaError_t launch_shape(const FewArgs &a, cudaStream_t st) {
     using S = FewShape<FMT, NT>;
-    static_assert(S::kSlots >= 4 && S::kSmem <= kFewSmem, "ring");
+    static_assert(S::kSlots >= 3 && S::kSmem <= kFewSmem, "ring");
     static_assert(S::kSlotBytes % 1024 == 0, "swizzled boxes need 1024-byte aligned slots");
     FewMaps m;
     const uint64_t E = a.E, I = a.I, H = a.H, Is = a.Is;
@@ -766,8 +839,8 @@ cudaError_t launch_shape(const FewArgs &a, cudaStream_t st) {
     p.h = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(a.h) + part_bytes(S::kTp));
     p.sync = a.sync;
     if (!encode_weights<FMT>(&m.gate, a.gate.w, E * I, H) || !encode_weights<FMT>(&m.up, a.up.w, E * I, H) ||
-        !encode_weights<FMT>(&m.down, a.down.w, E * H, I) || !encode_2d(&m.x, a.x, a.T, H, S::kTp) ||
-        !encode_2d(&m.h, p.h, 2 * S::kTp, p.ldh, 2 * S::kTp))
+        !encode_weights<FMT>(&m.down, a.down.w, E * H, I) || !encode_3d(&m.x, a.x, a.T, 2 * H, 128, S::kTp, 2 * S::kBoxes) ||
+        !encode_3d(&m.h, p.h, 2 * S::kTp, 2 * (uint64_t)p.ldh, 128, 2 * S::kTp, 2 * S::kBoxes))
         return cudaErrorInvalidValue;
     if (Is > 0) {
         if (!encode_weights<FMT>(&m.s_gate, a.s_gate.w, Is, H) || !encode_weights<FMT>(&m.s_up, a.s_up.w, Is, H) ||

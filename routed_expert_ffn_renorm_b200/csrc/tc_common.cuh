@@ -105,6 +105,14 @@ __device__ __forceinline__ void tma_load_2d_hint(const CUtensorMap *map, uint64_
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(policy)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_3d_hint(const CUtensorMap *map, uint64_t *bar, void *dst, int x, int y, int z,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+        "{%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+}
 // Untiled bulk copy global -> shared to a shared-memory address, completing on
 // an mbarrier (both addresses 16-byte aligned, bytes a multiple of 16).
 __device__ __forceinline__ void bulk_load_s(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -317,6 +325,25 @@ inline bool encode_2d_u8(CUtensorMap *m, const void *base, uint64_t rows, uint64
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE,
                     box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// A row-major matrix of row_bytes-byte rows as [row_bytes / chunk][rows][chunk]
+// bytes: box = chunk bytes (128 or 64, swizzled at that width) x box_rows rows x
+// box_chunks chunks.  row_bytes is a multiple of chunk; chunks behind the row's
+// last read as zeros.
+inline bool encode_3d(CUtensorMap *m, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t chunk,
+                      uint32_t box_rows, uint32_t box_chunks) {
+    auto fn = get_encode_fn();
+    if (!fn || (chunk != 128 && chunk != 64) || row_bytes % chunk != 0) return false;
+    cuuint64_t dims[3] = {chunk, rows, row_bytes / chunk};
+    cuuint64_t strides[2] = {row_bytes, chunk};
+    cuuint32_t box[3] = {chunk, box_rows, box_chunks};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    chunk == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
