@@ -48,7 +48,8 @@ using namespace tc;
 
 constexpr int kFewGroups = 4;                    // consumer groups: each takes a quarter of a step's columns
 constexpr int kFewConsumers = kFewGroups * 128;  // 4 warps of 32 weight rows per group
-constexpr int kFewThreads = kFewConsumers + 64;  // + weight producer, token producer
+constexpr int kFewRouters = 64;                  // routing threads beside a shared expert's phase
+constexpr int kFewThreads = kFewConsumers + 64 + kFewRouters;  // + weight producer, token producer
 constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;
 constexpr int kFewMaxSms = 160;
 constexpr int kFewSmem = 227 * 1024;
@@ -63,14 +64,15 @@ struct FewRouting {
     int nu, ndrop;
 };
 
-// Arrive on a grid barrier (one thread, after a barrier of the writers), and wait for all of the grid.
+// Arrive on a grid barrier (one thread, after a CTA barrier of the writers: its
+// fence is cumulative over what they wrote), and wait for all of the grid.
 __device__ __forceinline__ void grid_arrive(int32_t *ctr) {
     __threadfence();
     atomicAdd(ctr, 1);
 }
-__device__ __forceinline__ bool grid_wait(int32_t *ctr, volatile int *abort_flag, int32_t *status) {
+__device__ __forceinline__ bool grid_wait(int32_t *ctr, int arrivals, volatile int *abort_flag, int32_t *status) {
     const unsigned long long t0 = globaltimer();
-    while (ld_acquire(ctr) < (int)gridDim.x) {
+    while (ld_acquire(ctr) < arrivals) {
         if (*abort_flag) return false;
         if (globaltimer() - t0 > kWaitLimitNs) {
             *abort_flag = 1;
@@ -83,62 +85,131 @@ __device__ __forceinline__ bool grid_wait(int32_t *ctr, volatile int *abort_flag
 __device__ __forceinline__ void consumers_sync() { named_bar_sync(1, kFewConsumers); }
 
 template <int V>
-__device__ __noinline__ int few_route_token(int t, const FewArgs &a, FewRouting &r, int lane) {
-    return route_token<V, false>(t, a.E, a.k, a.norm_topk, a.topp, a.logits, r.idx, r.w, nullptr, lane);
+__device__ __noinline__ int few_route_token(int t, const FewArgs &a, const float *row, FewRouting &r, int lane) {
+    return route_token<V, false>(0, a.E, a.k, a.norm_topk, a.topp, row, r.idx + t * a.k, r.w + t * a.k, nullptr, lane);
 }
 
-// Route all tokens, apply the budget, list the experts in use (all consumer warps).
-__device__ void few_route(const FewArgs &a, FewRouting &r) {
-    const int tid = threadIdx.x, nthr = kFewConsumers, lane = tid & 31, Tk = a.T * a.k;
-    for (int t = tid >> 5; t < a.T; t += nthr >> 5) {
-        int c;
-        if (a.E <= 128)
-            c = few_route_token<4>(t, a, r, lane);
-        else if (a.E <= 256)
-            c = few_route_token<8>(t, a, r, lane);
-        else if (a.E <= 512)
-            c = few_route_token<16>(t, a, r, lane);
-        else
-            c = few_route_token<32>(t, a, r, lane);
-        if (lane == 0) r.keff[t] = c;
+// K splits of the projection: the grid over groups of 8 experts, a split no
+// narrower than one 64-wide block per warp; one where the consumers route and
+// the rows' sums would not fit in their `floats` of shared memory.
+constexpr int kFewMaxSplits = 8;
+__device__ __forceinline__ int few_splits(const FewArgs &a, int floats) {
+    if (a.Is == 0 && a.T * a.E > floats) return 1;  // a row per consumer warp
+    const int blocks = (a.H / 64 + kFewConsumers / 32 - 1) / (kFewConsumers / 32);
+    return max(1, min(min((int)gridDim.x / ((a.E + 7) / 8), blocks), kFewMaxSplits));
+}
+
+// Route token t (one warp).  splits > 1: its logits are that many partials at
+// `lpart`, added here in `row` (E floats of the warp).
+__device__ void few_route_one(int t, const FewArgs &a, FewRouting &r, int splits, const float *lpart, float *row,
+                              bool keep, int lane) {
+    const float *logits = a.logits + (size_t)t * a.E;
+    if (splits > 1) {
+        for (int e0 = lane; e0 < a.E; e0 += 128) {
+            float s[4] = {};
+#pragma unroll 4
+            for (int i = 0; i < splits; ++i) {
+                const float *src = lpart + ((size_t)i * a.T + t) * a.E;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[j] += __ldcg(src + min(e0 + 32 * j, a.E - 1));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (e0 + 32 * j < a.E) {
+                    row[e0 + 32 * j] = s[j];
+                    if (keep) a.logits[(size_t)t * a.E + e0 + 32 * j] = s[j];
+                }
+        }
+        __syncwarp();
+        logits = row;
     }
+    int c;
+    if (a.E <= 128)
+        c = few_route_token<4>(t, a, logits, r, lane);
+    else if (a.E <= 256)
+        c = few_route_token<8>(t, a, logits, r, lane);
+    else if (a.E <= 512)
+        c = few_route_token<16>(t, a, logits, r, lane);
+    else
+        c = few_route_token<32>(t, a, logits, r, lane);
+    if (lane == 0) r.keff[t] = c;
+    __syncwarp();
+}
+
+// Every token routed by this CTA: the warps of `nthr` threads, a token each.
+__device__ __noinline__ void few_route_all(const FewArgs &a, FewRouting &r, int splits, const float *lpart, float *rows,
+                                           int tid, int nthr) {
+    for (int t = tid >> 5; t < a.T; t += nthr >> 5)
+        few_route_one(t, a, r, splits, lpart, rows + (tid >> 5) * a.E, blockIdx.x == 0, tid & 31);
+}
+
+// Every token routed by one CTA of the grid and read by all (64 threads): `picks`
+// holds [T] kept counts, [T k] experts, [T k] weights; `ctr` counts the tokens.
+__device__ __noinline__ void few_route_shared(const FewArgs &a, FewRouting &r, int splits, const float *lpart, float *row,
+                                              int32_t *picks, int32_t *ctr, int tid, volatile int *abort_flag) {
+    const int lane = tid & 31, Tk = a.T * a.k;
+    if (tid < 32)
+        for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+            few_route_one(t, a, r, splits, lpart, row, true, lane);
+            for (int s = lane; s < a.k; s += 32) {
+                __stcg(picks + a.T + t * a.k + s, r.idx[t * a.k + s]);
+                __stcg(picks + a.T + Tk + t * a.k + s, __float_as_int(r.w[t * a.k + s]));
+            }
+            if (lane == 0) __stcg(picks + t, r.keff[t]);
+            __syncwarp();
+            if (lane == 0) {
+                __threadfence();
+                atomicAdd(ctr, 1);
+            }
+        }
+    if (tid == 0) grid_wait(ctr, a.T, abort_flag, a.status);
+    named_bar_sync(5, kFewRouters);
+    for (int s = tid; s < Tk; s += kFewRouters) {
+        r.idx[s] = __ldcg(picks + a.T + s);
+        r.w[s] = __int_as_float(__ldcg(picks + a.T + Tk + s));
+    }
+    if (tid < a.T) r.keff[tid] = __ldcg(picks + tid);
+}
+
+// Apply the budget to the routed tokens and list the experts in use: threads
+// tid < nthr that meet on barrier `bar`.
+__device__ __noinline__ void few_choose(const FewArgs &a, FewRouting &r, int tid, int nthr, int bar) {
+    const int lane = tid & 31, Tk = a.T * a.k;
+    auto sync = [&] { named_bar_sync(bar, nthr); };
     for (int e = tid; e < kMaxExperts; e += nthr) r.mask[e] = 0;
-    consumers_sync();
+    sync();
     for (int s = tid; s < Tk; s += nthr)
         if (r.idx[s] >= 0 && r.idx[s] < a.E) atomicOr(&r.mask[r.idx[s]], 1u << (s / a.k));
-    consumers_sync();
+    sync();
     int mine = 0;
     for (int e = tid; e < a.E; e += nthr) mine += r.mask[e] != 0;
     if (tid == 0) r.nu = 0;
-    consumers_sync();
+    sync();
     if (mine) atomicAdd(&r.nu, mine);
-    consumers_sync();
+    sync();
     const int nu = r.nu;
     const bool cut = a.budget > 0 && nu > a.budget;
     if (cut) {
         // the sum of the weights routed to each expert, tokens then slots ascending
         for (int e = tid; e < a.E; e += nthr) {
             float s = 0.f;
-            if (r.mask[e])
-                for (int i = 0; i < Tk; ++i)
-                    if (r.idx[i] == e) s += r.w[i];
-            r.agg[e] = s;
+#pragma unroll 8
+            for (int i = 0; i < Tk; ++i) s += r.idx[i] == e ? r.w[i] : 0.f;
+            r.agg[e] = r.mask[e] ? s : -1.f;
         }
-        consumers_sync();
+        sync();
         // rank in (sum descending, id ascending); the others leave
-        bool drop[kMaxExperts / kFewConsumers];
-        int n = 0;
-        for (int e = tid; e < a.E; e += nthr, ++n) {
+        for (int e = tid; e < a.E; e += nthr) {
             int rank = 0;
-            for (int o = 0; o < a.E; ++o)
-                rank += r.mask[o] != 0 && (r.agg[o] > r.agg[e] || (r.agg[o] == r.agg[e] && o < e));
-            drop[n] = r.mask[e] == 0 || rank >= a.budget;
+            const float mine = r.agg[e];
+#pragma unroll 8
+            for (int o = 0; o < a.E; ++o) {
+                const float other = r.agg[o];
+                rank += (other > mine) | ((other == mine) & (o < e));
+            }
+            if (rank >= a.budget) r.mask[e] = 0;
         }
-        consumers_sync();
-        n = 0;
-        for (int e = tid; e < a.E; e += nthr, ++n)
-            if (drop[n]) r.mask[e] = 0;
-        consumers_sync();
+        sync();
         for (int t = tid; t < a.T; t += nthr) {
             int32_t *ti = r.idx + t * a.k;
             float *tw = r.w + t * a.k;
@@ -164,7 +235,7 @@ __device__ void few_route(const FewArgs &a, FewRouting &r) {
             r.keff[t] = c;
         }
     }
-    consumers_sync();
+    sync();
     if (tid < 32) {
         int n = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
@@ -178,7 +249,7 @@ __device__ void few_route(const FewArgs &a, FewRouting &r) {
             r.ndrop = nu - n;
         }
     }
-    consumers_sync();
+    sync();
     if (blockIdx.x == 0) {  // the routing's optional outputs
         for (int s = tid; s < Tk; s += nthr) {
             if (a.idx) a.idx[s] = r.idx[s];
@@ -221,7 +292,8 @@ struct FewShape {
     static constexpr int kSlotBytes = kTokOff + 2 * kXBytes;
     static constexpr int kPartFloats = 256 * NT * 4;  // one row block's sums: 8 tiles of 16 rows x 32 lanes
     static constexpr int kXchFloats = kFewGroups * kPartFloats > 16 * 128 ? kFewGroups * kPartFloats : 16 * 128;
-    static constexpr int kFixed = 1024 + (int)sizeof(FewRouting) + kXchFloats * 4 + 1024;
+    static constexpr int kRowFloats = kMaxExperts;
+    static constexpr int kFixed = 1024 + (int)sizeof(FewRouting) + (kXchFloats + kRowFloats) * 4 + 1024;
     static constexpr int kSlots = (kFewSmem - kFixed) / kSlotBytes;
     static constexpr int kSmem = kFixed + kSlots * kSlotBytes;
 };
@@ -232,18 +304,29 @@ struct __align__(64) FewMaps {
 
 struct FewPlan {
     FewArgs a;
+    float *lpart;  // [kFewMaxSplits][T, E] partial logits
+    int32_t *picks;  // [T] kept counts, [T k] experts, [T k] weights
     uint16_t *h;   // [2 Tp, ldh] bf16: h, then its remainder
     int ldh;
     float *part;   // [3][kFewMaxSms][2] row-block partials
-    int32_t *sync; // [0], [1] grid barriers, [2] CTAs done, [16 + phase * kFewMaxSms + cta] partial arrivals
+    int32_t *sync; // [0], [1] grid barriers, [2] CTAs done, [3] tokens routed, [16 + phase * kFewMaxSms + cta] partial arrivals
 };
 
 // This CTA's share of a phase: steps [lo, hi) of `total`, `per` to a row block.
+// Whole row blocks where that keeps no CTA busier than equal shares do by more
+// than the 3 us that adding partials takes, about five steps.
+constexpr int kFewSplitSteps = 5;
 struct Share {
     int per, total, ctas, lo, hi;
     __device__ Share(int units, int per_unit) : per(per_unit), total(units * per_unit) {
         ctas = min((int)gridDim.x, total);
         lo = hi = 0;
+        const int most = (units + (int)gridDim.x - 1) / (int)gridDim.x;  // whole units for the busiest CTA
+        if (most * per <= total / (int)gridDim.x + kFewSplitSteps) {
+            lo = min(units, (int)blockIdx.x * most) * per;
+            hi = min(units, ((int)blockIdx.x + 1) * most) * per;
+            return;
+        }
         if ((int)blockIdx.x < ctas) {
             lo = (int)((long long)blockIdx.x * total / ctas);
             hi = (int)((long long)(blockIdx.x + 1) * total / ctas);
@@ -429,7 +512,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *xch = reinterpret_cast<float *>(ring + (size_t)kSlots * S::kSlotBytes);  // group 1's sums; projection sums
-    FewRouting &r = *reinterpret_cast<FewRouting *>(xch + S::kXchFloats);
+    FewRouting &r = *reinterpret_cast<FewRouting *>(xch + S::kXchFloats + S::kRowFloats);
     uint64_t *fullw = reinterpret_cast<uint64_t *>((reinterpret_cast<uintptr_t>(&r + 1) + 7) & ~uintptr_t(7));
     uint64_t *fullb = fullw + kSlots, *empty = fullb + kSlots, *routed = empty + kSlots;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(routed + 1);
@@ -525,7 +608,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 if (phase == 1 && !mbar_wait(routed, 0, abort_flag, a.status, true)) break;
                 const Share sh = share(phase);
                 if (phase == 2) {
-                    if (!grid_wait(p.sync + 1, abort_flag, a.status)) break;
+                    if (!grid_wait(p.sync + 1, (int)gridDim.x, abort_flag, a.status)) break;
                     fence_proxy_async_global();  // h was written by ordinary stores
                 }
                 const CUtensorMap *map = phase == 2 ? &maps.h : &maps.x;
@@ -554,6 +637,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             }
             for (uint32_t n = issued > (uint32_t)kSlots ? issued - kSlots : 0; n < issued; ++n)
                 mbar_wait(&fullb[n % kSlots], (n / kSlots) & 1u, abort_flag, a.status, false);
+        }
+    } else if (warp >= kFewConsumers / 32 + 2) {
+        // ================= routers =================
+        // With a shared expert, the wait for everyone's logits and the routing hide
+        // behind its gate/up stream: each token is routed by one CTA of the grid, and
+        // all read the picks.  Without one the consumers, idle till then, route every
+        // token in every CTA: 16 warps, a token each, and one grid barrier less.
+        if (a.Is > 0) {
+            const int tid = threadIdx.x - kFewConsumers - 64;
+            if (a.project && tid == 0) grid_wait(p.sync, (int)gridDim.x, abort_flag, a.status);
+            named_bar_sync(5, kFewRouters);
+            few_route_shared(a, r, a.project ? few_splits(a, S::kXchFloats) : 1, p.lpart, xch + S::kXchFloats, p.picks,
+                             p.sync + 3, tid, abort_flag);
+            few_choose(a, r, tid, kFewRouters, 5);
+            if (tid == 0) mbar_arrive(routed);
         }
     } else {
         // ================= consumers =================
@@ -584,22 +682,27 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 }
                 consumers_sync();
             }
+        const int splits = a.project ? few_splits(a, S::kXchFloats) : 1;
         if (a.project) {
-            // logits: eight experts (the mma's columns) per CTA, tokens its rows, the
-            // warps on alternate 64-wide K blocks; lane (g, q) holds 16 consecutive
-            // columns 16 q of rows g and g + 8, the same permutation of K on both sides
-            const int g = lane >> 2, q = lane & 3;
-            for (int o = cta; o < (a.E + 7) / 8; o += gridDim.x) {
+            // logits: eight experts (the mma's columns) and a K split per CTA, tokens its
+            // rows, the warps on alternate 64-wide K blocks; lane (g, q) holds 16
+            // consecutive columns 16 q of rows g and g + 8, the same permutation of K on
+            // both sides
+            const int g = lane >> 2, q = lane & 3, groups = (a.E + 7) / 8;
+            for (int item = cta; item < groups * splits; item += gridDim.x) {
+                const int o = item % groups, sp = item / groups;
+                const int kb0 = a.H / 64 * sp / splits, kb1 = a.H / 64 * (sp + 1) / splits;
                 const uint16_t *x0 = a.x + (size_t)min(g, a.T - 1) * a.H, *x1 = a.x + (size_t)min(g + 8, a.T - 1) * a.H;
                 const uint16_t *w0 = a.w_router + (size_t)min(o * 8 + g, a.E - 1) * a.H;
                 float d[4] = {};
 #pragma unroll 3
-                for (int kb = warp; kb < a.H / 64; kb += kFewConsumers / 32) {
+                for (int kb = kb0 + warp; kb < kb1; kb += kFewConsumers / 32) {
                     const int k = kb * 64 + q * 16;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint4 u = __ldg(reinterpret_cast<const uint4 *>(x0 + k) + i);
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x1 + k) + i);
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);  // tokens 8 .. 15
+                        if (NT > 1) v = __ldg(reinterpret_cast<const uint4 *>(x1 + k) + i);
                         const uint4 w = __ldg(reinterpret_cast<const uint4 *>(w0 + k) + i);
                         mma16816(d, u.x, v.x, u.y, v.y, w.x, w.y);
                         mma16816(d, u.z, v.z, u.w, v.w, w.z, w.w);
@@ -612,18 +715,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                     float v = 0.f;
                     for (int w = 0; w < kFewConsumers / 32; ++w) v += xch[w * 128 + tid];
                     const int t = tid >> 3, e = o * 8 + (tid & 7);
-                    if (t < a.T && e < a.E) a.logits[(size_t)t * a.E + e] = v;
+                    float *dst = splits > 1 ? p.lpart + (size_t)sp * a.T * a.E : a.logits;
+                    if (t < a.T && e < a.E) dst[(size_t)t * a.E + e] = v;
                 }
                 consumers_sync();
             }
-            if (tid == 0) {
-                grid_arrive(p.sync);
-                grid_wait(p.sync, abort_flag, a.status);
-            }
-            consumers_sync();
+            if (tid == 0) grid_arrive(p.sync);
         }
-        few_route(a, r);
-        if (tid == 0) mbar_arrive(routed);
+        if (a.Is == 0) {
+            if (a.project) {
+                if (tid == 0) grid_wait(p.sync, (int)gridDim.x, abort_flag, a.status);
+                consumers_sync();
+            }
+            few_route_all(a, r, splits, p.lpart, xch, tid, kFewConsumers);
+            few_choose(a, r, tid, kFewConsumers, 1);
+            if (tid == 0) mbar_arrive(routed);
+        }
 
         const int grp = warp >> 2, rg = warp & 3, g = lane >> 2, q = lane & 3;
         const int sub = grp >> 1, half = grp & 1;  // this group's columns: a half of a chunk of the step
@@ -633,6 +740,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
         for (int n = 0; n < NT; ++n) sg[n][0] = sg[n][1] = 0.f;
         for (int phase = 0; phase < 3; ++phase) {
+            if (phase == 1 && a.Is > 0) dead |= !mbar_wait(routed, 0, abort_flag, a.status, true);
             const Share sh = share(phase);
             int unit = sh.lo / max(sh.per, 1), at = sh.lo - unit * sh.per, left = sh.hi - sh.lo;
             bool have_sg = false;
@@ -729,9 +837,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             __stcg(slot(cta) + n * 256, make_float4(sum[n][0], sum[n][1], sum[n][2], sum[n][3]));
-                        __threadfence();
                         named_bar_sync(4, 256);
                         if (tid == 0) {
+                            __threadfence();
                             int32_t *ctr = p.sync + 16 + phase * kFewMaxSms + first;
                             const bool is_last = atomicAdd(ctr, 1) == last - first;
                             if (is_last) *ctr = 0;
@@ -743,15 +851,23 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                         if (whole) {
 #pragma unroll
                             for (int n = 0; n < NT; ++n) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0.f;
-                            for (int c = first; c <= last; ++c)
+                            for (int c0 = first; c0 <= last; c0 += 4) {  // four in flight, added in order
+                                float4 o[4][NT];
 #pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    const float4 o = __ldcg(slot(c) + n * 256);
-                                    sum[n][0] += o.x;
-                                    sum[n][1] += o.y;
-                                    sum[n][2] += o.z;
-                                    sum[n][3] += o.w;
-                                }
+                                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) o[c][n] = __ldcg(slot(min(c0 + c, last)) + n * 256);
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    if (c0 + c <= last)
+#pragma unroll
+                                        for (int n = 0; n < NT; ++n) {
+                                            sum[n][0] += o[c][n].x;
+                                            sum[n][1] += o[c][n].y;
+                                            sum[n][2] += o[c][n].z;
+                                            sum[n][3] += o[c][n].w;
+                                        }
+                            }
                         }
                     }
                     if (whole && phase < 2) {
@@ -799,8 +915,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 ++unit;
             }
             if (phase == 1 && warp < 8) {  // this CTA's part of h is written
-                fence_proxy_async_global();
-                __threadfence();
                 named_bar_sync(4, 256);
                 if (tid == 0) grid_arrive(p.sync + 1);
             }
@@ -812,10 +926,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         p.sync[0] = 0;
         p.sync[1] = 0;
         p.sync[2] = 0;
+        p.sync[3] = 0;
     }
 }
 
 size_t part_bytes(int tp) { return (size_t)3 * kFewMaxSms * 2 * 128 * tp * 4; }
+size_t lpart_bytes(int T, int E) { return (size_t)kFewMaxSplits * T * E * 4; }
+size_t picks_bytes(int T, int k) { return (size_t)T * (2 * k + 1) * 4; }
+size_t route_bytes(int T, int E, int k) { return (lpart_bytes(T, E) + picks_bytes(T, k) + 255) / 256 * 256; }
 int few_ldh(int T, int E, int I, int k, int Is) { return Is + std::min(E, T * k) * I; }
 int few_tp(int T) { return T <= 8 ? 8 : 16; }
 
@@ -836,7 +954,9 @@ cudaError_t launch_shape(const FewArgs &a, cudaStream_t st) {
     p.a = a;
     p.ldh = few_ldh(a.T, a.E, a.I, a.k, a.Is);
     p.part = static_cast<float *>(a.h);
-    p.h = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(a.h) + part_bytes(S::kTp));
+    p.lpart = reinterpret_cast<float *>(static_cast<uint8_t *>(a.h) + part_bytes(S::kTp));
+    p.h = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(a.h) + part_bytes(S::kTp) + route_bytes(a.T, a.E, a.k));
+    p.picks = reinterpret_cast<int32_t *>(p.lpart) + lpart_bytes(a.T, a.E) / 4;
     p.sync = a.sync;
     if (!encode_weights<FMT>(&m.gate, a.gate.w, E * I, H) || !encode_weights<FMT>(&m.up, a.up.w, E * I, H) ||
         !encode_weights<FMT>(&m.down, a.down.w, E * H, I) || !encode_3d(&m.x, a.x, a.T, 2 * H, 128, S::kTp, 2 * S::kBoxes) ||
@@ -880,7 +1000,7 @@ cudaError_t launch_fmt(const FewArgs &a, cudaStream_t st) {
 
 size_t few_scratch_bytes(int T, int E, int I, int k, int Is) {
     const int tp = few_tp(T);
-    return part_bytes(tp) + (size_t)2 * tp * few_ldh(T, E, I, k, Is) * 2;
+    return part_bytes(tp) + route_bytes(T, E, k) + (size_t)2 * tp * few_ldh(T, E, I, k, Is) * 2;
 }
 
 cudaError_t launch_few(const FewArgs &a, int fmt, cudaStream_t st) {
