@@ -61,7 +61,7 @@ struct FewRouting {
     uint32_t mask[kMaxExperts];  // tokens of each expert
     float agg[kMaxExperts];
     uint16_t list[kFewMaxSlots];  // experts in use, ascending
-    int nu, ndrop;
+    int nu;
 };
 
 // Arrive on a grid barrier (one thread, after a CTA barrier of the writers: its
@@ -84,68 +84,112 @@ __device__ __forceinline__ bool grid_wait(int32_t *ctr, int arrivals, volatile i
 }
 __device__ __forceinline__ void consumers_sync() { named_bar_sync(1, kFewConsumers); }
 
-template <int V>
-__device__ __noinline__ int few_route_token(int t, const FewArgs &a, const float *row, FewRouting &r, int lane) {
-    return route_token<V, false>(0, a.E, a.k, a.norm_topk, a.topp, row, r.idx + t * a.k, r.w + t * a.k, nullptr, lane);
-}
-
 // K splits of the projection: the grid over groups of 8 experts, a split no
-// narrower than one 64-wide block per warp; one where the consumers route and
-// the rows' sums would not fit in their `floats` of shared memory.
+// narrower than one 64-wide block per warp.
 constexpr int kFewMaxSplits = 8;
-__device__ __forceinline__ int few_splits(const FewArgs &a, int floats) {
-    if (a.Is == 0 && a.T * a.E > floats) return 1;  // a row per consumer warp
+__device__ __forceinline__ int few_splits(const FewArgs &a) {
     const int blocks = (a.H / 64 + kFewConsumers / 32 - 1) / (kFewConsumers / 32);
     return max(1, min(min((int)gridDim.x / ((a.E + 7) / 8), blocks), kFewMaxSplits));
 }
 
-// Route token t (one warp).  splits > 1: its logits are that many partials at
-// `lpart`, added here in `row` (E floats of the warp).
-__device__ void few_route_one(int t, const FewArgs &a, FewRouting &r, int splits, const float *lpart, float *row,
-                              bool keep, int lane) {
-    const float *logits = a.logits + (size_t)t * a.E;
-    if (splits > 1) {
-        for (int e0 = lane; e0 < a.E; e0 += 128) {
-            float s[4] = {};
-#pragma unroll 4
-            for (int i = 0; i < splits; ++i) {
-                const float *src = lpart + ((size_t)i * a.T + t) * a.E;
+// Route token t (one warp): the decisions of route_token, written as short loops
+// over a row of keys in shared memory, as this code runs once per token and cold.
+// Lane l owns experts l + 32 i, so the row needs no barrier.  splits > 1: the
+// logits are that many partials at `lpart`.  `row`: kFewRowWords words, the keys
+// and a stage for the loads, so that a round trip to L2 (1 to 2 us beside the
+// weight stream) fetches 32 values per lane.
+constexpr int kFewRowWords = 2 * kMaxExperts;
+__device__ __forceinline__ void few_route_one(int t, const FewArgs &a, FewRouting &r, int splits, const float *lpart,
+                                           uint32_t *row, bool keep, int lane) {
+    const int E = a.E, k = a.k;
+    const float *src = splits > 1 ? lpart + (size_t)t * E : a.logits + (size_t)t * E;
+    const int slots = (E + 31) >> 5, batch = 32 / min(splits, 32);  // slots per round trip: batch splits <= 32 loads
+    float *stage = reinterpret_cast<float *>(row + kMaxExperts) + lane;
+    uint32_t km = 0;
+#pragma unroll 1
+    for (int j0 = 0; j0 < slots; j0 += batch) {
+        const int nj = min(batch, slots - j0), n = nj * splits;
+        float v[32];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] += __ldcg(src + min(e0 + 32 * j, a.E - 1));
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (e0 + 32 * j < a.E) {
-                    row[e0 + 32 * j] = s[j];
-                    if (keep) a.logits[(size_t)t * a.E + e0 + 32 * j] = s[j];
-                }
+        for (int f = 0; f < 32; ++f) {
+            const int g = min(f, n - 1), i = g / nj, e = lane + 32 * (j0 + g - i * nj);
+            v[f] = __ldcg(src + (size_t)i * a.T * E + min(e, E - 1));
         }
-        __syncwarp();
-        logits = row;
+#pragma unroll
+        for (int f = 0; f < 32; ++f) stage[f * 32] = v[f];
+#pragma unroll 1
+        for (int j = 0; j < nj; ++j) {
+            float s = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < splits; ++i) s += stage[(i * nj + j) * 32];
+            const int e = lane + 32 * (j0 + j);
+            if (e < E) {
+                const uint32_t key = float_order_key(s);
+                km = max(km, key);
+                row[e] = key;
+                if (keep && splits > 1) a.logits[(size_t)t * E + e] = s;
+            }
+        }
     }
-    int c;
-    if (a.E <= 128)
-        c = few_route_token<4>(t, a, logits, r, lane);
-    else if (a.E <= 256)
-        c = few_route_token<8>(t, a, logits, r, lane);
-    else if (a.E <= 512)
-        c = few_route_token<16>(t, a, logits, r, lane);
-    else
-        c = few_route_token<32>(t, a, logits, r, lane);
+    const float m = order_key_float(__reduce_max_sync(0xffffffffu, km));
+    float s = 0.f;
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32) s += expf(order_key_float(row[e]) - m);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    int my_idx = -1;
+    uint32_t my_key = 0u;
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) {  // the largest key, the lowest id among equal ones
+        uint32_t best = 0u, at = 0xffffffffu;
+#pragma unroll 4
+        for (int e = lane; e < E; e += 32) {
+            const uint32_t key = row[e];
+            if (key > best) {
+                best = key;
+                at = e;
+            }
+        }
+        const uint32_t kmax = __reduce_max_sync(0xffffffffu, best);
+        const int win = (int)__reduce_min_sync(0xffffffffu, best == kmax ? at : 0xffffffffu);
+        if ((win & 31) == lane) row[win] = 0u;
+        if (lane == j) {
+            my_idx = win;
+            my_key = kmax;
+        }
+    }
+    float p = lane < k ? expf(order_key_float(my_key) - m) / s : 0.f;
+    auto normalise = [&](int n) {  // by the sum of the first n, in slot order
+        float sum = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) sum += __shfl_sync(0xffffffffu, p, j);
+        p = p / sum;
+    };
+    if (a.norm_topk) normalise(k);
+    int c = k;  // kept slots
+    if (a.topp > 0.f && a.topp < 1.f) {
+        float mass = __shfl_sync(0xffffffffu, p, 0);  // the same in every lane
+        for (c = 1; c < k && mass < a.topp; ++c) mass += __shfl_sync(0xffffffffu, p, c);
+        if (a.norm_topk && c < k) normalise(c);
+    }
+    if (lane < k) {
+        r.idx[t * k + lane] = lane < c ? my_idx : -1;
+        r.w[t * k + lane] = lane < c ? p : 0.f;
+    }
     if (lane == 0) r.keff[t] = c;
     __syncwarp();
 }
 
-// Every token routed by this CTA: the warps of `nthr` threads, a token each.
-__device__ __noinline__ void few_route_all(const FewArgs &a, FewRouting &r, int splits, const float *lpart, float *rows,
-                                           int tid, int nthr) {
-    for (int t = tid >> 5; t < a.T; t += nthr >> 5)
-        few_route_one(t, a, r, splits, lpart, rows + (tid >> 5) * a.E, blockIdx.x == 0, tid & 31);
+// Every token routed by this CTA, a warp each.
+__device__ __forceinline__ void few_route_all(const FewArgs &a, FewRouting &r, int splits, const float *lpart,
+                                              uint32_t *rows, int warp, int lane) {
+    for (int t = warp; t < a.T; t += kFewConsumers / 32)
+        few_route_one(t, a, r, splits, lpart, rows + warp * kFewRowWords, blockIdx.x == 0, lane);
 }
 
 // Every token routed by one CTA of the grid and read by all (64 threads): `picks`
 // holds [T] kept counts, [T k] experts, [T k] weights; `ctr` counts the tokens.
-__device__ __noinline__ void few_route_shared(const FewArgs &a, FewRouting &r, int splits, const float *lpart, float *row,
+__device__ __forceinline__ void few_route_shared(const FewArgs &a, FewRouting &r, int splits, const float *lpart, uint32_t *row,
                                               int32_t *picks, int32_t *ctr, int tid, volatile int *abort_flag) {
     const int lane = tid & 31, Tk = a.T * a.k;
     if (tid < 32)
@@ -173,41 +217,49 @@ __device__ __noinline__ void few_route_shared(const FewArgs &a, FewRouting &r, i
 
 // Apply the budget to the routed tokens and list the experts in use: threads
 // tid < nthr that meet on barrier `bar`.
-__device__ __noinline__ void few_choose(const FewArgs &a, FewRouting &r, int tid, int nthr, int bar) {
+__device__ __forceinline__ void few_choose(const FewArgs &a, FewRouting &r, int tid, int nthr, int bar) {
     const int lane = tid & 31, Tk = a.T * a.k;
     auto sync = [&] { named_bar_sync(bar, nthr); };
-    for (int e = tid; e < kMaxExperts; e += nthr) r.mask[e] = 0;
+    auto list = [&] {  // the experts with tokens, ascending
+        if (tid < 32) {
+            int n = 0;
+            for (int e0 = 0; e0 < a.E; e0 += 32) {
+                const bool in = e0 + lane < a.E && r.mask[e0 + lane] != 0;
+                const unsigned b = __ballot_sync(0xffffffffu, in);
+                if (in) r.list[n + __popc(b & ((1u << lane) - 1u))] = (uint16_t)(e0 + lane);
+                n += __popc(b);
+            }
+            if (lane == 0) r.nu = n;
+        }
+        sync();
+    };
+    for (int e = tid; e < a.E; e += nthr) r.mask[e] = 0;
     sync();
     for (int s = tid; s < Tk; s += nthr)
         if (r.idx[s] >= 0 && r.idx[s] < a.E) atomicOr(&r.mask[r.idx[s]], 1u << (s / a.k));
     sync();
-    int mine = 0;
-    for (int e = tid; e < a.E; e += nthr) mine += r.mask[e] != 0;
-    if (tid == 0) r.nu = 0;
-    sync();
-    if (mine) atomicAdd(&r.nu, mine);
-    sync();
+    list();
     const int nu = r.nu;
-    const bool cut = a.budget > 0 && nu > a.budget;
-    if (cut) {
+    if (a.budget > 0 && nu > a.budget) {
         // the sum of the weights routed to each expert, tokens then slots ascending
-        for (int e = tid; e < a.E; e += nthr) {
+        for (int u = tid; u < nu; u += nthr) {
+            const int e = r.list[u];
             float s = 0.f;
 #pragma unroll 8
             for (int i = 0; i < Tk; ++i) s += r.idx[i] == e ? r.w[i] : 0.f;
-            r.agg[e] = r.mask[e] ? s : -1.f;
+            r.agg[u] = s;
         }
         sync();
         // rank in (sum descending, id ascending); the others leave
-        for (int e = tid; e < a.E; e += nthr) {
+        for (int u = tid; u < nu; u += nthr) {
             int rank = 0;
-            const float mine = r.agg[e];
+            const float mine = r.agg[u];
 #pragma unroll 8
-            for (int o = 0; o < a.E; ++o) {
+            for (int o = 0; o < nu; ++o) {
                 const float other = r.agg[o];
-                rank += (other > mine) | ((other == mine) & (o < e));
+                rank += (other > mine) | ((other == mine) & (o < u));
             }
-            if (rank >= a.budget) r.mask[e] = 0;
+            if (rank >= a.budget) r.mask[r.list[u]] = 0;
         }
         sync();
         for (int t = tid; t < a.T; t += nthr) {
@@ -234,22 +286,8 @@ __device__ __noinline__ void few_choose(const FewArgs &a, FewRouting &r, int tid
             }
             r.keff[t] = c;
         }
+        list();
     }
-    sync();
-    if (tid < 32) {
-        int n = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const bool in = e0 + lane < a.E && r.mask[e0 + lane] != 0;
-            const unsigned b = __ballot_sync(0xffffffffu, in);
-            if (in) r.list[n + __popc(b & ((1u << lane) - 1u))] = (uint16_t)(e0 + lane);
-            n += __popc(b);
-        }
-        if (lane == 0) {
-            r.nu = n;
-            r.ndrop = nu - n;
-        }
-    }
-    sync();
     if (blockIdx.x == 0) {  // the routing's optional outputs
         for (int s = tid; s < Tk; s += nthr) {
             if (a.idx) a.idx[s] = r.idx[s];
@@ -259,7 +297,7 @@ __device__ __noinline__ void few_choose(const FewArgs &a, FewRouting &r, int tid
             if (a.keff) a.keff[t] = r.keff[t];
         if (a.budget > 0 && a.kept)
             for (int e = tid; e < a.E; e += nthr) a.kept[e] = r.mask[e] != 0;
-        if (a.budget > 0 && a.n_dropped && tid == 0) *a.n_dropped = r.ndrop;
+        if (a.budget > 0 && a.n_dropped && tid == 0) *a.n_dropped = nu - r.nu;
     }
 }
 
@@ -292,7 +330,7 @@ struct FewShape {
     static constexpr int kSlotBytes = kTokOff + 2 * kXBytes;
     static constexpr int kPartFloats = 256 * NT * 4;  // one row block's sums: 8 tiles of 16 rows x 32 lanes
     static constexpr int kXchFloats = kFewGroups * kPartFloats > 16 * 128 ? kFewGroups * kPartFloats : 16 * 128;
-    static constexpr int kRowFloats = kMaxExperts;
+    static constexpr int kRowFloats = kFewRowWords;
     static constexpr int kFixed = 1024 + (int)sizeof(FewRouting) + (kXchFloats + kRowFloats) * 4 + 1024;
     static constexpr int kSlots = (kFewSmem - kFixed) / kSlotBytes;
     static constexpr int kSmem = kFixed + kSlots * kSlotBytes;
@@ -506,7 +544,8 @@ __device__ __forceinline__ void few_step(float (&acc)[2][NT][4], uint32_t slot, 
 }
 
 template <int FMT, int NT>
-__global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewMaps maps, const FewPlan p) {
+__global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewMaps maps,
+                                                             const __grid_constant__ FewPlan p) {
     using S = FewShape<FMT, NT>;
     constexpr int kTp = S::kTp, kSlots = S::kSlots;
     extern __shared__ uint8_t smem_raw[];
@@ -648,7 +687,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             const int tid = threadIdx.x - kFewConsumers - 64;
             if (a.project && tid == 0) grid_wait(p.sync, (int)gridDim.x, abort_flag, a.status);
             named_bar_sync(5, kFewRouters);
-            few_route_shared(a, r, a.project ? few_splits(a, S::kXchFloats) : 1, p.lpart, xch + S::kXchFloats, p.picks,
+            few_route_shared(a, r, a.project ? few_splits(a) : 1, p.lpart, 
+                             reinterpret_cast<uint32_t *>(xch + S::kXchFloats), p.picks,
                              p.sync + 3, tid, abort_flag);
             few_choose(a, r, tid, kFewRouters, 5);
             if (tid == 0) mbar_arrive(routed);
@@ -682,7 +722,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 }
                 consumers_sync();
             }
-        const int splits = a.project ? few_splits(a, S::kXchFloats) : 1;
+        const int splits = a.project ? few_splits(a) : 1;
         if (a.project) {
             // logits: eight experts (the mma's columns) and a K split per CTA, tokens its
             // rows, the warps on alternate 64-wide K blocks; lane (g, q) holds 16
@@ -727,7 +767,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 if (tid == 0) grid_wait(p.sync, (int)gridDim.x, abort_flag, a.status);
                 consumers_sync();
             }
-            few_route_all(a, r, splits, p.lpart, xch, tid, kFewConsumers);
+            // in the ring, which is empty till the routed experts are known
+            few_route_all(a, r, splits, p.lpart, reinterpret_cast<uint32_t *>(ring), warp, lane);
+            fence_proxy_async_shared();
+            consumers_sync();
             few_choose(a, r, tid, kFewConsumers, 1);
             if (tid == 0) mbar_arrive(routed);
         }
@@ -947,6 +990,7 @@ template <int FMT, int NT>
 cudaError_t launch_shape(const FewArgs &a, cudaStream_t st) {
     using S = FewShape<FMT, NT>;
     static_assert(S::kSlots >= 3 && S::kSmem <= kFewSmem, "ring");
+    static_assert(S::kSlots * S::kSlotBytes >= kFewConsumers / 32 * kFewRowWords * 4, "routing rows in the ring");
     static_assert(S::kSlotBytes % 1024 == 0, "swizzled boxes need 1024-byte aligned slots");
     FewMaps m;
     const uint64_t E = a.E, I = a.I, H = a.H, Is = a.Is;
