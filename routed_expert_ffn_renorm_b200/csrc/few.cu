@@ -103,25 +103,25 @@ __device__ __forceinline__ void few_route_one(int t, const FewArgs &a, FewRoutin
                                            uint32_t *row, bool keep, int lane) {
     const int E = a.E, k = a.k;
     const float *src = splits > 1 ? lpart + (size_t)t * E : a.logits + (size_t)t * E;
-    const int slots = (E + 31) >> 5, batch = 32 / min(splits, 32);  // slots per round trip: batch splits <= 32 loads
+    const int slots = (E + 31) >> 5;
+    const int lg = 5 - (splits > 1) - (splits > 2) - (splits > 4), nj = 1 << lg;  // slots per round trip: 32 loads
     float *stage = reinterpret_cast<float *>(row + kMaxExperts) + lane;
     uint32_t km = 0;
 #pragma unroll 1
-    for (int j0 = 0; j0 < slots; j0 += batch) {
-        const int nj = min(batch, slots - j0), n = nj * splits;
+    for (int j0 = 0; j0 < slots; j0 += nj) {
         float v[32];
 #pragma unroll
         for (int f = 0; f < 32; ++f) {
-            const int g = min(f, n - 1), i = g / nj, e = lane + 32 * (j0 + g - i * nj);
-            v[f] = __ldcg(src + (size_t)i * a.T * E + min(e, E - 1));
+            const int i = min(f >> lg, splits - 1), e = lane + 32 * (j0 + (f & (nj - 1)));
+            v[f] = __ldcg(src + i * a.T * E + min(e, E - 1));
         }
 #pragma unroll
         for (int f = 0; f < 32; ++f) stage[f * 32] = v[f];
 #pragma unroll 1
-        for (int j = 0; j < nj; ++j) {
+        for (int j = 0; j < min(nj, slots - j0); ++j) {
             float s = 0.f;
 #pragma unroll 4
-            for (int i = 0; i < splits; ++i) s += stage[(i * nj + j) * 32];
+            for (int i = 0; i < splits; ++i) s += stage[((i << lg) + j) * 32];
             const int e = lane + 32 * (j0 + j);
             if (e < E) {
                 const uint32_t key = float_order_key(s);
