@@ -19,6 +19,7 @@ import ctypes
 import os
 import threading
 from dataclasses import dataclass
+from functools import cached_property
 from typing import Optional
 
 __all__ = [
@@ -105,9 +106,13 @@ class MoEConfig:
     budget: int = 0
     topp: float = 0.0  # per-token top-p trim; 0 (or >= 1) = off
 
-    def _c(self) -> _Config:
+    @cached_property
+    def _struct(self) -> _Config:
         return _Config(self.hidden, self.n_routed_experts, self.moe_intermediate_size, self.num_experts_per_tok,
                        self.shared_intermediate_size, int(bool(self.norm_topk)), self.budget, float(self.topp))
+
+    def _c(self) -> _Config:
+        return self._struct
 
 
 @dataclass
@@ -187,6 +192,7 @@ class MoEWeightsNVFP4:
         return _WeightsNVFP4(*(_ptr(getattr(self, n), allow_none=True) for n, _ in _WeightsNVFP4._fields_))
 
 
+_torch_module = None  # imported by the first call that takes a tensor
 _lib = None
 _checked = None
 _lock = threading.Lock()
@@ -199,6 +205,8 @@ def load_library(build_if_stale: bool = True, variant: str = "release"):
     inputs, reported as MOE_STATUS_BOUNDS); the functions below always call
     the release library unless a test swaps it in."""
     global _lib, _checked
+    if variant == "release" and _lib is not None:
+        return _lib
     with _lock:
         if variant == "release" and _lib is not None:
             return _lib
@@ -261,19 +269,26 @@ def load_library(build_if_stale: bool = True, variant: str = "release"):
         return lib
 
 
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _ptr(t, allow_none: bool = False):
     if t is None:
         if allow_none:
             return None
         raise ValueError("tensor argument is None")
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
     if not t.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _expect(t, dtype, numel: int, name: str):
@@ -285,9 +300,10 @@ def _expect(t, dtype, numel: int, name: str):
 
 
 def _stream(stream):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # torch.cuda.current_stream() without building the Stream object: 4 us of a 15 us call
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(fn: str, rc: int):
@@ -570,22 +586,21 @@ def moe_forward(cfg: MoEConfig, x, logits, weights: MoEWeights, out, ws, *, aux:
 
 
 def _expect_like(t, dtype, shape, device, name: str):
-    """Host-side check of one tensor of a call: type, shape and device."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on "
+    """Host-side check of one tensor of a call: type, shape (a tuple) and device index."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on cuda:{device}, got {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}")
 
 
 def _current_device(t, name: str):
-    """The launch goes to the current device: its tensors have to live there."""
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+    """The launch goes to the current device (its index is returned): its tensors have to live there."""
+    if not t.is_cuda or t.get_device() != _torch()._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_torch().cuda.current_device()}")
+    return t.get_device()
 
 
 def _forward_few(fn: str, cfg: MoEConfig, x, logits, weights, out, ws, aux, stream):
-    import torch
+    torch = _torch()
     dev = _current_device(x, "x")
     T, H, E, I, Is = x.shape[0], cfg.hidden, cfg.n_routed_experts, cfg.moe_intermediate_size, \
         cfg.shared_intermediate_size
@@ -640,7 +655,7 @@ def moe_linear(x, w, out, ws, *, bias=None, activation: str = "none", residual=N
     """out [T, N] = residual + act(x [T, K] . w [N, K]^T + bias): bf16 in, out
     bf16 or fp32 by its type; activation "none", "relu", "gelu" (erf) or
     "silu"; out may be `residual` itself."""
-    import torch
+    torch = _torch()
     dev = _current_device(x, "x")
     (T, K), N = x.shape, w.shape[0]
     _expect_like(x, torch.bfloat16, (T, K), dev, "x")
@@ -667,7 +682,7 @@ def moe_verify(target_probs, draft_tokens, accept_u, sample_u, tokens, n_accepte
     n_accepted [B] how many stayed.  draft_probs [B, L, V], or None for a
     drafter that puts all its mass on its token; draft_len [B] for blocks
     shorter than L."""
-    import torch
+    torch = _torch()
     dev = _current_device(target_probs, "target_probs")
     B, L1, V = target_probs.shape
     L = L1 - 1

@@ -346,7 +346,8 @@ struct FewPlan {
     int32_t *picks;  // [T] kept counts, [T k] experts, [T k] weights
     uint16_t *h;   // [2 Tp, ldh] bf16: h, then its remainder
     int ldh;
-    float *part;   // [3][kFewMaxSms][2] row-block partials
+    float *part;   // [2][kFewMaxSms][2] row-block partials: the down projection's lie over the
+                   // shared expert's, which the grid barrier has seen added up
     int32_t *sync; // [0], [1] grid barriers, [2] CTAs done, [3] tokens routed, [16 + phase * kFewMaxSms + cta] partial arrivals
 };
 
@@ -874,7 +875,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                         const int first = sh.owner(unit * sh.per), last = sh.owner(unit * sh.per + sh.per - 1);
                         auto slot = [&](int c) {
                             return reinterpret_cast<float4 *>(
-                                       p.part + (size_t)((phase * kFewMaxSms + c) * 2 + (c == first)) * S::kPartFloats) +
+                                       p.part + (size_t)(((phase & 1) * kFewMaxSms + c) * 2 + (c == first)) * S::kPartFloats) +
                                    wr * 32 + lane;
                         };
 #pragma unroll
@@ -973,7 +974,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     }
 }
 
-size_t part_bytes(int tp) { return (size_t)3 * kFewMaxSms * 2 * 128 * tp * 4; }
+size_t part_bytes(int tp) { return (size_t)2 * kFewMaxSms * 2 * 128 * tp * 4; }
 size_t lpart_bytes(int T, int E) { return (size_t)kFewMaxSplits * T * E * 4; }
 size_t picks_bytes(int T, int k) { return (size_t)T * (2 * k + 1) * 4; }
 size_t route_bytes(int T, int E, int k) { return (lpart_bytes(T, E) + picks_bytes(T, k) + 255) / 256 * 256; }

@@ -60,10 +60,9 @@ WsLayout ws_layout(const moe_config_t &c, int T) {
     L.ybuf = take((size_t)T * (c.num_experts_per_tok + 1) * c.hidden * 2);
     L.logits = take((size_t)T * E * 4);
     L.rpart = take(rp_partial_bytes(T, (int)E, c.hidden));
-    L.few = T <= kFewMaxTokens
-                ? take(few_scratch_bytes(T, (int)E, c.moe_intermediate_size, c.num_experts_per_tok,
-                                   c.shared_intermediate_size))
-                : off;
+    // every workspace also serves the few-token layer with fewer tokens
+    L.few = take(few_scratch_bytes(std::min(T, kFewMaxTokens), (int)E, c.moe_intermediate_size, c.num_experts_per_tok,
+                                   c.shared_intermediate_size));
     L.total = off;
     return L;
 }

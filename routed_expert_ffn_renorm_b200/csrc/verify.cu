@@ -10,8 +10,9 @@
 // A cluster of 8 CTAs per request, no workspace: every CTA decides the
 // block's length itself (2 L gathered probabilities), sums its eighth of the
 // vocabulary row, and the eight totals meet through distributed shared
-// memory; the CTA whose range holds u total scans its warps' sums and then the
-// one warp's segment again (from L2).  The row is read from HBM once: 8 V bytes
+// memory; the CTA whose range holds u total scans its warps' sums, the warp that
+// holds it the sums it kept of its segment's eighths, and only that eighth is
+// read again (from L2).  The row is read from HBM once: 8 V bytes
 // per request, the bound for large batches; a small one is bound by the chain
 // token -> p(x) -> row -> exchange -> segment.
 //
@@ -30,6 +31,7 @@ using namespace tc;
 constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerCluster = 8;
+constexpr int kVerSubs = 8;  // parts of a warp's segment whose sums it keeps
 
 struct VerArgs {
     int B, L, V;
@@ -45,25 +47,26 @@ struct VerRow {
     int hot;  // token whose q is 1 (q == null), -1: none
     bool pv, qv;
     __device__ void values(long long i, long long end, double (&r)[4]) const {
-        float a[4] = {}, b[4] = {};
-        load(p, pv, i, end, a);
-        if (q) load(q, qv, i, end, b);
+        mass(i, load4(p, pv, i, end), q ? load4(q, qv, i, end) : make_float4(0.f, 0.f, 0.f, 0.f), r);
+    }
+    __device__ void mass(long long i, const float4 &a, const float4 &b, double (&r)[4]) const {
+        const float x[4] = {a.x, a.y, a.z, a.w};
+        float y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            if (i + c == hot) b[c] = 1.f;
-            const double d = (double)a[c] - (double)b[c];
+            if (i + c == hot) y[c] = 1.f;
+            const double d = (double)x[c] - (double)y[c];
             r[c] = d > 0. && d <= 3.5e38 ? d : 0.;
         }
     }
-    __device__ static void load(const float *s, bool vec, long long i, long long end, float (&v)[4]) {
-        if (vec && i + 4 <= end) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(s + i));
-            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-        } else {
+    // values i .. i + 3, those from `end` on 0
+    __device__ static float4 load4(const float *s, bool vec, long long i, long long end) {
+        if (vec && i + 4 <= end) return __ldg(reinterpret_cast<const float4 *>(s + i));
+        float v[4] = {};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (i + c < end) v[c] = __ldg(s + i + c);
-        }
+        for (int c = 0; c < 4; ++c)
+            if (i + c < end) v[c] = __ldg(s + i + c);
+        return make_float4(v[0], v[1], v[2], v[3]);
     }
 };
 
@@ -79,13 +82,15 @@ __device__ __forceinline__ double ld_cluster_f64(uint32_t cluster_addr) {
     return v;
 }
 
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerArgs a) {
+__global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerArgs a) {
     __shared__ double wsum[kVerWarps];
     __shared__ double total[2];  // this CTA's sum of the row, of p alone when the first is 0
     __shared__ int s_n, s_refused;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank(), b = blockIdx.x / kVerCluster;
     const int V = a.V, L = a.L;
+    pdl_launch_dependents();
+    pdl_wait();
 
     if (warp == 0) {  // the accepted length
         const int n_in = a.len ? min(max(__ldg(a.len + b), 0), L) : L;
@@ -128,15 +133,49 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerArgs a) {
     // this warp's segment: multiples of 128 values (one float4 per lane)
     const long long per = (((long long)V + kVerCluster * kVerWarps - 1) / (kVerCluster * kVerWarps) + 127) / 128 * 128;
     const long long s0 = min((long long)V, (rank * kVerWarps + warp) * per), s1 = min((long long)V, s0 + per);
-    double tot[kVerCluster], all = 0.;
+    const long long sub = (per / 128 + kVerSubs - 1) / kVerSubs * 128;  // and its eighths
+    double tot[kVerCluster], all = 0., sums[kVerSubs] = {};
     for (int pass = 0; pass < 2; ++pass) {
         double s = 0.;
+        if (sub == 128 && s0 + per <= V && row.pv && (!row.q || row.qv)) {
+            // a whole segment, aligned: one float4 per lane and eighth, four eighths in flight
+            const float4 *p4 = reinterpret_cast<const float4 *>(row.p + s0) + lane;
+            const float4 *q4 = reinterpret_cast<const float4 *>((row.q ? row.q : row.p) + s0) + lane;
+            const int n = (int)(per / 128);
+#pragma unroll
+            for (int k0 = 0; k0 < kVerSubs; k0 += 4) {
+                if (k0 >= n) break;
+                float4 pf[4], qf[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // behind the segment: its last eighth again, not counted
+                    pf[k] = __ldg(p4 + min(k0 + k, n - 1) * 32);
+                    qf[k] = __ldg(q4 + min(k0 + k, n - 1) * 32);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    double r[4];
+                    row.mass(s0 + (k0 + k) * 128 + lane * 4, pf[k], row.q ? qf[k] : make_float4(0.f, 0.f, 0.f, 0.f), r);
+                    sums[k0 + k] = k0 + k < n ? (r[0] + r[1]) + (r[2] + r[3]) : 0.;
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < kVerSubs; ++k) {
+                const long long e0 = min(s1, s0 + k * sub), e1 = min(s1, e0 + sub);
+                double t = 0.;
 #pragma unroll 4
-        for (long long i = s0 + lane * 4; i < s1; i += 128) {
-            double r[4];
-            row.values(i, s1, r);
-            s += (r[0] + r[1]) + (r[2] + r[3]);
+                for (long long i = e0 + lane * 4; i < e1; i += 128) {
+                    double r[4];
+                    row.values(i, s1, r);
+                    t += (r[0] + r[1]) + (r[2] + r[3]);
+                }
+#pragma unroll
+                for (int c = 0; c < kVerSubs; ++c)
+                    if (c == k) sums[c] = t;
+            }
         }
+#pragma unroll
+        for (int k = 0; k < kVerSubs; ++k) s += sums[k];
         s = warp_sum(s);
         if (lane == 0) wsum[warp] = s;
         __syncthreads();
@@ -196,12 +235,27 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerArgs a) {
             bw += wsum[w];
         }
         if (warp == ow) {
-            long long tok = -1, last = -1;
-            double run = wb;
-            for (long long i0 = s0; i0 < s1 && tok < 0; i0 += 128) {
+            // the eighth of the segment (rounding past the end: the last with mass)
+            double run = wb, bs = wb;
+            long long tok = -1, last = -1, e0 = s0, e1 = s1;
+            bool sf = false;
+            if (per > 2 * 128) {  // (two eighths are as quickly read as summed)
+#pragma unroll
+                for (int k = 0; k < kVerSubs; ++k) {
+                    const double t = warp_sum(sums[k]);
+                    if (!sf && t > 0.) {
+                        e0 = s0 + k * sub;
+                        run = bs;
+                        sf = bs + t > target;
+                    }
+                    bs += t;
+                }
+                e1 = min(s1, e0 + sub);
+            }
+            for (long long i0 = e0; i0 < e1 && tok < 0; i0 += 128) {
                 const long long i = i0 + lane * 4;
                 double r[4] = {};
-                if (i < s1) row.values(i, s1, r);
+                if (i < e1) row.values(i, s1, r);
                 const double mine = (r[0] + r[1]) + (r[2] + r[3]);
                 double incl = mine;
 #pragma unroll
@@ -246,13 +300,15 @@ cudaError_t launch_verify(int B, int L, int V, const float *p, const float *q, c
     cfg.gridDim = dim3((unsigned)B * kVerCluster);
     cfg.blockDim = dim3(kVerThreads);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kVerCluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, verify_kernel, a);
 }
 
