@@ -11,6 +11,11 @@
 // accumulator lives in TMEM, double buffered: a tile's epilogue runs under the
 // next one's products.
 //
+// The tensor cores truncate at every addition to an accumulator, 4 per slice: at
+// K = 5120 an fp32 result was 5.5e-6 off, 30 times an fp32 sum's error.  fp32 out
+// therefore sums segments of 512 columns in TMEM and the segments in registers,
+// rounded to nearest (5e-7); for bf16 out the rounding hides the rest.
+//
 // Bound: few tokens stream W from HBM (one CTA per SM, single tiles); from
 // about 200 tokens on the tensor cores bind, and a pair halves each CTA's share
 // of the token operand.
@@ -46,6 +51,7 @@ constexpr int kLinMaxSms = 160;                // no device has more SMs (worksp
 constexpr int kLinSliceA = 128 * 128;          // 128 rows of W x 64 columns
 constexpr int kLinRing = 216 * 1024;           // at most
 constexpr int kLinAccStride = 256;             // TMEM columns between the two accumulators
+constexpr int kLinSegment = 8;                 // K slices summed in TMEM for fp32 out
 constexpr int kLinBand = 8;                    // row tiles of a band
 constexpr int kLinMaxStages = 16;
 constexpr int kLinMaxSplit = 12;               // shares of a tile: at most 14 (unaligned ends), counted in 4 bits
@@ -118,10 +124,10 @@ __device__ __forceinline__ void lin_residual(const LinearArgs &a, int t0, int n,
 }
 
 // Channel n of `count` tokens from t0: the epilogue of the sums v, in fp32, rounded once.
-template <bool kFull>
+template <bool kF32, bool kFull>
 __device__ __forceinline__ void lin_store32(const LinearArgs &a, int t0, int count, int n, const float (&v)[32]) {
     const size_t o = (size_t)t0 * a.N + n, ld = a.N;
-    if (a.out_f32) {
+    if (kF32) {
         float *out = static_cast<float *>(a.out) + o;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -133,6 +139,7 @@ __device__ __forceinline__ void lin_store32(const LinearArgs &a, int t0, int cou
             if (kFull || i < count) out[i * ld] = f32_to_bf16_bits(v[i]);
     }
 }
+template <bool kF32>
 __device__ __forceinline__ void lin_epilogue(const LinearArgs &a, int t0, int count, int n, float bias,
                                              const uint32_t (&res)[32], float (&v)[32]) {
 #pragma unroll
@@ -152,14 +159,16 @@ __device__ __forceinline__ void lin_epilogue(const LinearArgs &a, int t0, int co
         for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(res[i] << 16);
     }
     if (n >= a.N) return;
-    if (count >= 32) lin_store32<true>(a, t0, 32, n, v);
-    else lin_store32<false>(a, t0, count, n, v);
+    if (count >= 32) lin_store32<kF32, true>(a, t0, 32, n, v);
+    else lin_store32<kF32, false>(a, t0, count, n, v);
 }
 
-template <bool kPair>
+// kF32: fp32 out, the K axis summed in segments of kLinSegment slices.
+template <bool kPair, bool kF32>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinPlan p) {
     constexpr int kSlices = kPair ? 1 : 2;  // K slices per stage: one barrier round trip for two small ones
+    constexpr int kBlocks = 2;              // kF32: 32-column blocks of a token tile per epilogue half
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[kLinMaxStages], empty[kLinMaxStages], tfull[2], tempty[2], mma_done;
@@ -270,14 +279,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             LinWalk walk(p, worker, workers);
             int st = 0;
             uint32_t ph = 0;
-            bool ok = true;
-            for (uint32_t it = 0; ok && walk.next(tile, k0, k1); ++it) {
+            bool ok = true, more = walk.next(tile, k0, k1);
+            for (uint32_t it = 0; ok && more; ++it) {
                 const uint32_t acc = it & 1u;
                 if (!mbar_wait_fast<kPair>(&tempty[acc], ((it >> 1) & 1u) ^ 1u, &abort_flag, a.status, true)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * kLinAccStride;
-                for (int k = k0; k < k1; k += kSlices) {
-                    const int n = min(kSlices, k1 - k);
+                const int end = kF32 ? min(k1, k0 + kLinSegment) : k1;
+                for (int k = k0; k < end; k += kSlices) {
+                    const int n = min(kSlices, end - k);
                     if (!mbar_wait_fast<kPair>(&full[st], ph, &abort_flag, a.status, true)) {
                         ok = false;
                         break;
@@ -304,6 +314,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 if (!ok) break;
                 if constexpr (kPair) umma_commit_pair(&tfull[acc]);
                 else umma_commit(&tfull[acc]);
+                k0 = end;
+                if (k0 >= k1) more = walk.next(tile, k0, k1);
             }
             if constexpr (kPair) umma_commit_pair_local(&mma_done);
             else umma_commit(&mma_done);
@@ -318,34 +330,72 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             else mbar_arrive(&tempty[acc]);
         };
         LinWalk walk(p, worker, workers);
-        for (uint32_t it = 0; walk.next(tile, k0, k1); ++it) {
-            const uint32_t acc = it & 1u;
+        for (uint32_t it = 0; walk.next(tile, k0, k1);) {
             int r, j;
             lin_tile(p, tile, r, j);
             const int n = (kPair ? r * 256 + (int)rank * 128 : r * 128) + row;
             const int t0 = j * p.Nt, cols = min(p.Nt, a.T - t0);
             const bool whole = k1 - k0 == p.nk;
             uint32_t next[32];  // the coming block's residual, read ahead of its sums
-            if (whole && half * 32 < cols) lin_residual(a, t0 + half * 32, n, next);
-            if (elected) go_flag = mbar_wait<kPair>(&tfull[acc], (it >> 1) & 1u, &abort_flag, a.status, true);
-            named_bar_sync(1, kLinEpi);
-            if (!go_flag) break;
-            tc_fence_after();
-            const float bias = a.bias && n < a.N ? bf16_bits_to_f32(__ldg(a.bias + n)) : 0.f;
-            const uint32_t tbase = tmem_base + acc * kLinAccStride + ((uint32_t)(q * 32) << 16);
-            if (whole) {
-                for (int c0 = half * 32; c0 < cols; c0 += 64) {
-                    uint32_t res[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) res[i] = next[i];
-                    if (c0 + 64 < cols) lin_residual(a, t0 + c0 + 64, n, next);
-                    float v[32];
-                    tmem_ld32(tbase + (uint32_t)c0, v);
-                    lin_epilogue(a, t0 + c0, cols - c0, n, bias, res, v);
-                }
-                tc_fence_before();
+            if (!kF32 && whole && half * 32 < cols) lin_residual(a, t0 + half * 32, n, next);
+            // the sums: in TMEM, or (kF32) of all segments but the last in registers
+            float sum[kF32 ? kBlocks : 1][32];
+            uint32_t acc = 0, tbase = 0;
+            bool go = true;
+#pragma unroll 1
+            for (int k = k0; k < k1; k += kF32 ? kLinSegment : k1 - k0, ++it) {
+                acc = it & 1u;
+                tbase = tmem_base + acc * kLinAccStride + ((uint32_t)(q * 32) << 16);
+                if (elected) go_flag = mbar_wait<kPair>(&tfull[acc], (it >> 1) & 1u, &abort_flag, a.status, true);
                 named_bar_sync(1, kLinEpi);
-                if (elected) release(acc);
+                go = go_flag;
+                if (!go) break;
+                tc_fence_after();
+                if constexpr (kF32) {
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b)
+                        if (half * 32 + 64 * b < p.Nt) {
+                            float v[32];
+                            tmem_ld32(tbase + (uint32_t)(half * 32 + 64 * b), v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) sum[b][i] = k == k0 ? v[i] : sum[b][i] + v[i];
+                        }
+                    tc_fence_before();
+                    named_bar_sync(1, kLinEpi);
+                    if (elected) release(acc);
+                }
+            }
+            if (!go) break;
+            auto done = [&] {  // the accumulator is read
+                if constexpr (!kF32) {
+                    tc_fence_before();
+                    named_bar_sync(1, kLinEpi);
+                    if (elected) release(acc);
+                }
+            };
+            const float bias = a.bias && n < a.N ? bf16_bits_to_f32(__ldg(a.bias + n)) : 0.f;
+            if (whole) {
+                if constexpr (kF32) {
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b) {
+                        const int c0 = half * 32 + 64 * b;
+                        if (c0 < cols) {
+                            lin_residual(a, t0 + c0, n, next);
+                            lin_epilogue<kF32>(a, t0 + c0, cols - c0, n, bias, next, sum[b]);
+                        }
+                    }
+                } else {
+                    for (int c0 = half * 32; c0 < cols; c0 += 64) {
+                        uint32_t res[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) res[i] = next[i];
+                        if (c0 + 64 < cols) lin_residual(a, t0 + c0 + 64, n, next);
+                        float v[32];
+                        tmem_ld32(tbase + (uint32_t)c0, v);
+                        lin_epilogue<kF32>(a, t0 + c0, cols - c0, n, bias, res, v);
+                    }
+                }
+                done();
                 continue;
             }
             // a share of the tile: its sums to the workspace, [column / 4][128 rows] float4
@@ -361,18 +411,25 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             // by block a count, and whoever counts last adds the block up.  The shares
             // start at different blocks, so that the adding falls to all of them.
             const int nb = (blocks - half + 1) / 2;
-            for (int c0 = half * 32; c0 < p.Nt; c0 += 64) {
-                float v[32];
-                tmem_ld32(tbase + (uint32_t)c0, v);
+            auto put = [&](int c0, const float (&v)[32]) {
                 float4 *dst = part(worker) + c0 / 4 * 128;
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     __stcg(dst + c * 128, make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
+            };
+            if constexpr (kF32) {
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b)
+                    if (half * 32 + 64 * b < p.Nt) put(half * 32 + 64 * b, sum[b]);
+            } else {
+                for (int c0 = half * 32; c0 < p.Nt; c0 += 64) {
+                    float v[32];
+                    tmem_ld32(tbase + (uint32_t)c0, v);
+                    put(c0, v);
+                }
             }
-            tc_fence_before();
             __threadfence();
-            named_bar_sync(1, kLinEpi);
-            if (elected) release(acc);
+            done();
             uint32_t *ctr = reinterpret_cast<uint32_t *>(a.sync) + ((first << kPair) + (int)rank) * 4 + q;
             for (int i = 0, at = nb * (worker - first) / (last - first + 1); i < nb; ++i, at = at + 1 < nb ? at + 1 : 0) {
                 const int blk = 2 * at + half, c0 = 32 * blk;
@@ -400,7 +457,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         v[4 * c + 3] += o.w;
                     }
                 }
-                if (c0 < cols) lin_epilogue(a, t0 + c0, cols - c0, n, bias, next, v);
+                if (c0 < cols) lin_epilogue<kF32>(a, t0 + c0, cols - c0, n, bias, next, v);
             }
         }
     }
@@ -423,18 +480,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // Single CTAs up to this many tokens, pairs above.
 constexpr int kLinSingleTokens = 64;
 
-// Token tile: the tokens in as few tiles of at most 256 as hold them, rounded up to 16.
-int lin_token_tile(int T) {
-    const int tiles = (T + 255) / 256;
+// Token tile: the tokens in as few tiles of at most 256 (fp32 out: 128, the sums a
+// thread holds) as hold them, rounded up to 16.
+int lin_token_tile(int T, bool f32) {
+    const int most = f32 ? 128 : 256, tiles = (T + most - 1) / most;
     return ((T + tiles - 1) / tiles + 15) / 16 * 16;
 }
 
-template <bool kPair>
+template <bool kPair, bool kF32>
 cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
     constexpr int kSlices = kPair ? 1 : 2;
     LinPlan p{};
     p.a = a;
-    p.Nt = lin_token_tile(a.T);
+    p.Nt = lin_token_tile(a.T, kF32);
     p.nk = (a.K + 63) / 64;
     p.rt = (a.N + (kPair ? 255 : 127)) / (kPair ? 256 : 128);
     p.tt = (a.T + p.Nt - 1) / p.Nt;
@@ -463,7 +521,7 @@ cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!attr_set[dev].load(std::memory_order_acquire)) {
         const cudaError_t e =
-            cudaFuncSetAttribute(linear_kernel<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kLinRing);
+            cudaFuncSetAttribute(linear_kernel<kPair, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kLinRing);
         if (e != cudaSuccess) return e;
         attr_set[dev].store(1, std::memory_order_release);
     }
@@ -481,7 +539,7 @@ cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kPair ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, linear_kernel<kPair>, m, p);
+    return cudaLaunchKernelEx(&cfg, linear_kernel<kPair, kF32>, m, p);
 }
 
 }  // namespace
@@ -489,13 +547,16 @@ cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
 size_t linear_scratch_bytes(int T, int N, int K) {
     (void)N;
     (void)K;
-    return T == 0 ? 0 : (size_t)kLinMaxSms * 2 * 128 * ((lin_token_tile(T) + 31) / 32 * 32) * 4;  // two partials per CTA
+    // two partials per CTA; a bf16 tile is never narrower than an fp32 one
+    return T == 0 ? 0 : (size_t)kLinMaxSms * 2 * 128 * ((lin_token_tile(T, false) + 31) / 32 * 32) * 4;
 }
 
 cudaError_t launch_linear(const LinearArgs &a, cudaStream_t st) {
     const int sms = std::min(device_sm_count(), kLinMaxSms);
     if (sms <= 0) return cudaErrorInvalidDevice;
-    return a.T <= kLinSingleTokens || sms < 2 ? launch_shape<false>(a, sms, st) : launch_shape<true>(a, sms, st);
+    if (a.T <= kLinSingleTokens || sms < 2)
+        return a.out_f32 ? launch_shape<false, true>(a, sms, st) : launch_shape<false, false>(a, sms, st);
+    return a.out_f32 ? launch_shape<true, true>(a, sms, st) : launch_shape<true, false>(a, sms, st);
 }
 
 }  // namespace moe
