@@ -340,8 +340,14 @@ struct __align__(64) FewMaps {
     CUtensorMap gate, up, down, s_gate, s_up, s_down, x, h;
 };
 
+// Left shifts as factors (see the decoders below).
+struct FewShifts {
+    uint32_t by2, by4, by6, by8, by12;  // 1 << 2, ...
+};
+
 struct FewPlan {
     FewArgs a;
+    FewShifts shifts;
     float *lpart;  // [kFewMaxSplits][T, E] partial logits
     int32_t *picks;  // [T] kept counts, [T k] experts, [T k] weights
     uint16_t *h;   // [2 Tp, ldh] bf16: h, then its remainder
@@ -422,7 +428,7 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel) {
 // 2^(120 + se) finishes it; codes (2i, 2i + 1) of word j give pair 2j + i.
 // That factor is a bf16 while se <= 7 (weights below 2^16); larger scales take
 // the scalar decoder.
-__device__ __forceinline__ void decode16_mx(uint32_t (&v)[8], const uint32_t (&c)[4], uint32_t scale) {
+__device__ __forceinline__ void decode16_mx(uint32_t (&v)[8], const uint32_t (&c)[4], uint32_t scale, uint32_t by4) {
     if (__builtin_expect(scale <= 134u, 1)) {
         const uint32_t f = (scale + 120u) * 0x00800080u;
 #pragma unroll
@@ -430,7 +436,7 @@ __device__ __forceinline__ void decode16_mx(uint32_t (&v)[8], const uint32_t (&c
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t x = prmt(c[j], i ? 0xB3A2u : 0x9180u);  // a code and its sign, eight times, in each half
-                v[2 * j + i] = mul_bf16x2((x << 4) & 0x87F087F0u, f);
+                v[2 * j + i] = mul_bf16x2((x * by4) & 0x87F087F0u, f);
             }
     } else {
 #pragma unroll
@@ -443,19 +449,24 @@ __device__ __forceinline__ void decode16_mx(uint32_t (&v)[8], const uint32_t (&c
     }
 }
 // E2M1: likewise the value times 2^-126; the factor holds the E4M3 block scale
-// times 2^118, the missing 2^8 goes to the matrix scale.  Word j's pairs are
-// codes (i, i + 4), i = 0..3, so that one shift and mask extracts both.
+// (not negative) times 2^118 -- the code's bits in a bf16's fields are s 2^-120,
+// two products with 2^119 make the rest -- and the missing 2^8 goes to the matrix
+// scale.  Word j's pairs are codes (i, i + 4), i = 0..3.  The integer pipe paces
+// the decoding, so the shifts to the left are multiplications, on the other pipe;
+// by parameters, as constants would be made shifts again.
 constexpr float kNvFix = 256.f;
-__device__ __forceinline__ void decode16_nv(uint32_t (&v)[8], const uint32_t (&c)[2], uint32_t scale) {
-    const float sb = quant::e4m3_decode((uint8_t)scale) * 0x1p118f;  // exact: 4 significant bits
-    const uint32_t f = __byte_perm(__float_as_uint(sb), 0, 0x3232);
+__device__ __forceinline__ void decode16_nv(uint32_t (&v)[8], const uint32_t (&c)[2], uint32_t scale, const FewShifts &sh) {
+    constexpr uint32_t c119 = ((127u + 119u) << 7) * 0x00010001u;
+    const uint32_t f = mul_bf16x2(mul_bf16x2(scale * 0x00100010u, c119), c119);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t w = c[j], w8 = w >> 8;
+        const uint32_t mag[4] = {w * sh.by6, w * sh.by2, w8 * sh.by6, w8 * sh.by2};
+        const uint32_t sgn[4] = {w * sh.by12, w * sh.by8, w * sh.by4, w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t mag = i < 2 ? c[j] << (6 - 4 * i) : c[j] >> (4 * i - 6);
-            v[4 * j + i] = mul_bf16x2((mag & 0x01C001C0u) | ((c[j] << (12 - 4 * i)) & 0x80008000u), f);
-        }
+        for (int i = 0; i < 4; ++i)
+            v[4 * j + i] = mul_bf16x2((mag[i] & 0x01C001C0u) | (sgn[i] & 0x80008000u), f);
+    }
 }
 
 // One warp's share of a step: 32 weight rows (tiles 2 rg and 2 rg + 1) times a
@@ -463,7 +474,8 @@ __device__ __forceinline__ void decode16_nv(uint32_t (&v)[8], const uint32_t (&c
 // tiles are 16 consecutive rows and the token operand is h and its remainder;
 // otherwise a tile is 8 gate rows and the 8 up rows of the same channels.
 template <int FMT, int NT, bool kDown>
-__device__ __forceinline__ void few_step(float (&acc)[2][NT][4], uint32_t slot, int rg, int sub, int half, int lane) {
+__device__ __forceinline__ void few_step(float (&acc)[2][NT][4], uint32_t slot, int rg, int sub, int half, int lane,
+                                         const FewShifts &sh) {
     using S = FewShape<FMT, NT>;
     constexpr int kParts = kDown ? 2 : 1, kBoxBytes = kParts * S::kTp * 128;
     const int g = lane >> 2, q = lane & 3;
@@ -513,11 +525,11 @@ __device__ __forceinline__ void few_step(float (&acc)[2][NT][4], uint32_t slot, 
                 if constexpr (FMT == 1) {
                     uint32_t c[4];
                     lds128(c, wb + rr * 128 + (((half * 4 + q) ^ (rr & 7)) << 4));
-                    decode16_mx(v[m][hi], c, lds8(sc + rr * 4 + half * 2 + (q >> 1)));
+                    decode16_mx(v[m][hi], c, lds8(sc + rr * 4 + half * 2 + (q >> 1)), sh.by4);
                 } else {
                     uint32_t c[2];
                     lds64(c, wb + rr * 64 + (((half * 2 + (q >> 1)) ^ ((rr >> 1) & 3)) << 4) + (q & 1) * 8);
-                    decode16_nv(v[m][hi], c, lds8(sc + rr * 8 + half * 4 + q));
+                    decode16_nv(v[m][hi], c, lds8(sc + rr * 8 + half * 4 + q), sh);
                 }
             }
 #pragma unroll
@@ -833,8 +845,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                     }
                     if (live) {
                         const uint32_t slot = smem_u32(ring + (size_t)st * S::kSlotBytes);
-                        if (phase == 2) few_step<FMT, NT, true>(acc, slot, rg, sub, half, lane);
-                        else few_step<FMT, NT, false>(acc, slot, rg, sub, half, lane);
+                        if (phase == 2) few_step<FMT, NT, true>(acc, slot, rg, sub, half, lane, p.shifts);
+                        else few_step<FMT, NT, false>(acc, slot, rg, sub, half, lane, p.shifts);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&empty[st]);
@@ -997,6 +1009,7 @@ cudaError_t launch_shape(const FewArgs &a, cudaStream_t st) {
     const uint64_t E = a.E, I = a.I, H = a.H, Is = a.Is;
     FewPlan p;
     p.a = a;
+    p.shifts = {1u << 2, 1u << 4, 1u << 6, 1u << 8, 1u << 12};
     p.ldh = few_ldh(a.T, a.E, a.I, a.k, a.Is);
     p.part = static_cast<float *>(a.h);
     p.lpart = reinterpret_cast<float *>(static_cast<uint8_t *>(a.h) + part_bytes(S::kTp));
