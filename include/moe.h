@@ -423,7 +423,7 @@ int moe_forward(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const f
  *   - T > MOE_FEW_MAX_TOKENS returns MOE_ERR_UNSUPPORTED.
  *   - aux->counts, offsets, perm and slot_pos must be NULL (nothing is
  *     dispatched).  aux->logits receives projected logits, as in moe_forward.
- *   - Uses the workspace of moe_workspace_bytes(cfg, T), zeroed once
+ *   - Uses the workspace of moe_workspace_bytes(cfg, T' >= T), zeroed once
  *     (moe_status_clear); a launch leaves its counters at zero.  One workspace
  *     serves one stream at a time.
  *   - The kernel is a cooperative launch of one block per SM (its blocks wait
@@ -448,8 +448,12 @@ int moe_forward_few_nvfp4(const moe_config_t *cfg, int32_t T, const moe_bf16_t *
  * at all (out_f32 = 1: e.g. a head's logits).
  *   x [T, K]; w [N, K]; bias [N] or NULL; residual [T, N] or NULL; out [T, N]
  *   bf16 or f32.  activation: MOE_ACT_* (GELU is the erf form).
- *   - T >= 0 (0: no-op), N >= 1, K >= 8 a multiple of 8, T * N and N * K below
- *     2^40; any other size is as good (no multiple of a tile is asked for).
+ *   - T >= 0 (0: no-op), N >= 1, K >= 8 a multiple of 8, each at most 2^31 - 512,
+ *     T * N and N * K below 2^40; any other size is as good (no multiple of a tile
+ *     is asked for).
+ *   - The tensor cores truncate their sums; fp32 out therefore leaves them every
+ *     512 columns (4.5e-7 relative, as an fp32 product).
+ *   - The result is the same bits on every run on the same GPU model.
  *   - out may be `residual` itself (bf16), in place; it must not overlap
  *     anything else.
  *   - ws: moe_linear_workspace_bytes(T, N, K) bytes (0 for bad sizes), zeroed
@@ -484,7 +488,8 @@ int moe_linear(int32_t T, int32_t N, int32_t K, const moe_bf16_t *x, const moe_b
  *   - A refused token whose row has p <= q everywhere (rounded inputs) is
  *     drawn from p; a row without any mass gives -1.
  *   - sample_u below 0 or NaN counts as 0.
- *   - B = 0 is a no-op; L >= 0; V >= 1; B < 2^27.  No workspace. */
+ *   - B = 0 is a no-op; 0 <= L <= 2^20; V >= 1; B < 2^27.  No workspace.
+ *   - tokens and n_accepted must not overlap an input. */
 int moe_verify(int32_t B, int32_t L, int32_t V, const float *target_probs, const float *draft_probs,
                const int32_t *draft_tokens, const int32_t *draft_len, const float *accept_u, const float *sample_u,
                int32_t *tokens, int32_t *n_accepted, void *stream);

@@ -612,9 +612,13 @@ def _forward_few(fn: str, cfg: MoEConfig, x, logits, weights, out, ws, aux, stre
         raise ValueError("logits is None and the weights have no w_router")
     else:
         _expect_like(weights.w_router, torch.bfloat16, (E, H), dev, "w_router")
-    if weights.w_gate.shape[:2] != (E, I) or weights.w_down.shape[:2] != (E, H):
+    per = {"moe_forward_few": 1, "moe_forward_few_mxfp8": 1, "moe_forward_few_nvfp4": 2}[fn]  # weights per element
+    if weights.w_gate.shape != (E, I, H // per) or weights.w_up.shape != (E, I, H // per) or \
+            weights.w_down.shape != (E, H, I // per):
         raise ValueError("the expert weights' shapes differ from the configuration's")
-    if Is and (weights.ws_gate is None or weights.ws_gate.shape[0] != Is):
+    if Is and (weights.ws_gate is None or weights.ws_gate.shape != (Is, H // per) or
+               weights.ws_up.shape != (Is, H // per) or weights.ws_down.shape != (H, Is // per) or
+               weights.ws_gate_vec.shape != (H,)):
         raise ValueError("the shared expert's weights differ from the configuration's")
     w, a = weights._c(), _Aux()
     for name, t in (aux or {}).items():

@@ -124,7 +124,7 @@ __device__ __forceinline__ void few_route_one(int t, const FewArgs &a, FewRoutin
             for (int i = 0; i < splits; ++i) s += stage[((i << lg) + j) * 32];
             const int e = lane + 32 * (j0 + j);
             if (e < E) {
-                const uint32_t key = float_order_key(s);
+                const uint32_t key = max(float_order_key(s), 1u);  // 0 marks a chosen expert; only the NaN of all ones has it
                 km = max(km, key);
                 row[e] = key;
                 if (keep && splits > 1) a.logits[(size_t)t * E + e] = s;

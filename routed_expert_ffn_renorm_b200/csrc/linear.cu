@@ -483,8 +483,8 @@ constexpr int kLinSingleTokens = 64;
 // Token tile: the tokens in as few tiles of at most 256 (fp32 out: 128, the sums a
 // thread holds) as hold them, rounded up to 16.
 int lin_token_tile(int T, bool f32) {
-    const int most = f32 ? 128 : 256, tiles = (T + most - 1) / most;
-    return ((T + tiles - 1) / tiles + 15) / 16 * 16;
+    const int most = f32 ? 128 : 256, tiles = (T - 1) / most + 1;
+    return ((T - 1) / tiles + 16) / 16 * 16;
 }
 
 template <bool kPair, bool kF32>
@@ -494,8 +494,8 @@ cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
     p.a = a;
     p.Nt = lin_token_tile(a.T, kF32);
     p.nk = (a.K + 63) / 64;
-    p.rt = (a.N + (kPair ? 255 : 127)) / (kPair ? 256 : 128);
-    p.tt = (a.T + p.Nt - 1) / p.Nt;
+    p.rt = (a.N - 1) / (kPair ? 256 : 128) + 1;
+    p.tt = (a.T - 1) / p.Nt + 1;
     const long long tiles = (long long)p.rt * p.tt;
     if (tiles >= (1ll << 30)) return cudaErrorInvalidValue;
     int workers = kPair ? sms / 2 : sms;

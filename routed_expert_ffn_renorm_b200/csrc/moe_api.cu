@@ -755,9 +755,13 @@ int moe_forward_few_nvfp4(const moe_config_t *cfg, int32_t T, const moe_bf16_t *
 
 namespace {
 
+constexpr int32_t kLinearMaxSize = INT32_MAX - 511;  // a tile behind the last row or column keeps its index
+
 int check_linear(int32_t T, int32_t N, int32_t K) {
     if (T < 0 || N < 1 || K < 8) return MOE_ERR_INVALID_ARG;
-    if (K % 8 != 0 || (long long)T * N >= (1ll << 40) || (long long)N * K >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
+    if (K % 8 != 0 || T > kLinearMaxSize || N > kLinearMaxSize || K > kLinearMaxSize ||
+        (long long)T * N >= (1ll << 40) || (long long)N * K >= (1ll << 40))
+        return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

@@ -54,6 +54,22 @@ def test_few_refusals(fn):
         assert go(cfg=_cfg(moe_intermediate_size=192), n=1 << 40) == -2
 
 
+def test_a_workspace_serves_fewer_tokens():
+    lib = moe.load_library()
+    for kw in (dict(), dict(shared_intermediate_size=2048, hidden=5120, n_routed_experts=256)):
+        c = _cfg(**kw)
+        need = [lib.moe_workspace_bytes(ctypes.byref(c), T) for T in (1, 2, 8, 9, 15, 16, 17, 31, 64, 100, 1000)]
+        assert need == sorted(need)
+
+
+def test_linear_sizes_at_the_limits():
+    lib = moe.load_library()
+    most = 2 ** 31 - 512
+    assert lib.moe_linear_workspace_bytes(most, 1, 8) > 0 and lib.moe_linear_workspace_bytes(1, most, 8) > 0
+    for sizes in ((most + 1, 1, 8), (1, most + 1, 8), (1, 1, most + 8), (most, 1024, 8), (1, most, 1024)):
+        assert lib.moe_linear_workspace_bytes(*sizes) == 0
+
+
 def test_linear_refusals():
     lib = moe.load_library()
     need = lib.moe_linear_workspace_bytes(5, 7, 16)

@@ -127,6 +127,29 @@ def test_block_scaled_odd_blocks(fmt):
     check(cfg, inp, fmt)
 
 
+@pytest.mark.parametrize("kw", [dict(T=16, E=520, k=12, H=2048, I=64), dict(T=1, E=9, k=2, H=5120, I=64, Is=64),
+                                dict(T=16, E=600, k=8, H=3584, I=64, Is=128), dict(T=5, E=1024, k=32, H=1024, I=64, Is=64),
+                                dict(T=16, E=256, k=8, H=1152, I=64, Is=1024, budget=9, topp=0.8)],
+                         ids=lambda kw: "_".join(f"{a}{b}" for a, b in kw.items()))
+def test_projection_split_along_k(kw):
+    """The router's product cut along H over the CTAs, its routing with and without a shared expert."""
+    cfg = cfg_(**kw)
+    check(cfg, W.make_inputs(cfg, device="cuda", seed=15, router=True, gate_std=0.5), "bf16", None)
+
+
+def test_logits_of_all_ones_bits():
+    """Every logit the NaN of all ones: the experts are distinct and in range, other tokens unharmed."""
+    for Is in (0, 64):
+        cfg = cfg_(T=3, E=40, k=5, I=64, Is=Is)
+        inp = W.make_inputs(cfg, device="cuda", seed=16, gate_std=0.5)
+        good = run(cfg, inp)[0].clone()
+        inp.logits[1].view(torch.int32).fill_(-1)
+        idx = torch.empty(cfg.T, cfg.k, dtype=torch.int32, device="cuda")
+        out, _ = run(cfg, inp, aux={"topk_idx": idx})
+        assert torch.equal(out[[0, 2]], good[[0, 2]])
+        assert idx[1].tolist() == list(range(cfg.k))
+
+
 def test_equal_logits_keep_the_lower_expert():
     cfg = cfg_(T=4, E=70, k=5, I=64)
     inp = W.make_inputs(cfg, device="cuda", seed=6)
@@ -244,6 +267,11 @@ def test_binding_refusals():
         moe.moe_forward_few(c, inp.x, None, w, out, ws)  # no router projection either
     with pytest.raises(ValueError):
         moe.moe_forward_few(c, inp.x[:, ::2], inp.logits, w, out, ws)
+    for name in ("w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down", "ws_gate_vec"):
+        bad = weights_of(inp)
+        setattr(bad, name, getattr(bad, name)[:-1])
+        with pytest.raises(ValueError):
+            moe.moe_forward_few(c, inp.x, inp.logits, bad, out, ws)
     with pytest.raises(moe.MoEError) as e:
         big = torch.zeros(17, cfg.H, dtype=torch.bfloat16, device="cuda")
         moe.moe_forward_few(c, big, torch.zeros(17, cfg.E, device="cuda"), w, big.clone(),

@@ -54,6 +54,20 @@ def test_linear(T, N, K, act, bias, residual, dtype):
     check(T, N, K, act, bias, residual, dtype)
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 300, 8192), (16, 256, 4096), (70, 384, 5128), (200, 128, 8192)])
+def test_fp32_out_keeps_the_sums(T, N, K):
+    """fp32 results leave the tensor cores every 512 columns: 32 additions to an
+    accumulator, each losing less than 2^-23 of the magnitudes added so far for
+    the sum and as much for aligning its products, then the segments' fp32 sum."""
+    x, w, _, _ = make(T, N, K, False, False, 8)
+    out = torch.empty(T, N, device="cuda")
+    moe.moe_linear(x, w, out, workspace(T, N, K))
+    want, mag = x.double() @ w.double().T, x.double().abs() @ w.double().abs().T
+    assert ((out.double() - want).abs() <= (2 * 32 + (K + 511) // 512 + 16) * ref.F32 * mag).all()
+    # half an ulp lost on average in each addition
+    assert float((out.double() - want).norm() / want.norm()) < 32 * 2.0 ** -24
+
+
 def test_large_values_and_activation_tails():
     for act in ("gelu", "silu", "relu"):
         x, w, b, _ = make(20, 96, 64, True, False, 3)
