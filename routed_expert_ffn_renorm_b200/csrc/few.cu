@@ -103,6 +103,11 @@ __device__ __forceinline__ int few_splits(const FewArgs &a) {
     return max(1, min(min((int)gridDim.x / ((a.E + 7) / 8), blocks), kFewMaxSplits));
 }
 
+// Four bytes from global (L2) to shared memory; visible to this thread after cp.async.wait_all.
+__device__ __forceinline__ void copy_async4(float *dst, const float *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // Route token t (one warp): the decisions of route_token, written as short loops
 // over a row of keys in shared memory, as this code runs once per token and cold.
 // Lane l owns experts l + 32 i, so the row needs no barrier.  splits > 1: the
@@ -115,23 +120,24 @@ __device__ __forceinline__ void few_route_one(int t, const FewArgs &a, FewRoutin
     const int E = a.E, k = a.k;
     const float *src = splits > 1 ? lpart + (size_t)t * E : a.logits + (size_t)t * E;
     const int slots = (E + 31) >> 5;
-    const int lg = 5 - (splits > 1) - (splits > 2) - (splits > 4), nj = 1 << lg;  // slots per round trip: 32 loads
+    // slots per round trip: a power of two, at most 32 loads
+    int lg = 0;
+    while ((1 << lg) < slots && (splits << (lg + 1)) <= 32) ++lg;
+    const int nj = 1 << lg;
     float *stage = reinterpret_cast<float *>(row + kMaxExperts) + lane;
     uint32_t km = 0;
 #pragma unroll 1
     for (int j0 = 0; j0 < slots; j0 += nj) {
-        float v[32];
-#pragma unroll
-        for (int f = 0; f < 32; ++f) {
-            const int i = min(f >> lg, splits - 1), e = lane + 32 * (j0 + (f & (nj - 1)));
-            v[f] = __ldcg(src + i * a.T * E + min(e, E - 1));
+#pragma unroll 1
+        for (int f = 0; f < splits << lg; ++f) {
+            const int e = lane + 32 * (j0 + (f & (nj - 1)));
+            copy_async4(stage + f * 32, src + (f >> lg) * a.T * E + min(e, E - 1));
         }
-#pragma unroll
-        for (int f = 0; f < 32; ++f) stage[f * 32] = v[f];
+        asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
         for (int j = 0; j < min(nj, slots - j0); ++j) {
             float s = 0.f;
-#pragma unroll 4
+#pragma unroll 1
             for (int i = 0; i < splits; ++i) s += stage[((i << lg) + j) * 32];
             const int e = lane + 32 * (j0 + j);
             if (e < E) {
