@@ -154,25 +154,43 @@ __device__ __forceinline__ void few_route_one(int t, const FewArgs &a, FewRoutin
     for (int e = lane; e < E; e += 32) s += expf(order_key_float(row[e]) - m);
 #pragma unroll
     for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    int my_idx = -1;
-    uint32_t my_key = 0u;
-#pragma unroll 1
-    for (int j = 0; j < k; ++j) {  // the largest key, the lowest id among equal ones
-        uint32_t best = 0u, at = 0xffffffffu;
+    // k rounds of the largest key, the lowest id among equal ones.  Each lane holds
+    // its two best; it looks through its row again when both are gone.
+    uint32_t best = 0u, at = 0xffffffffu, second = 0u, at2 = 0xffffffffu;
+    auto scan = [&] {
+        best = second = 0u;
+        at = at2 = 0xffffffffu;
 #pragma unroll 4
         for (int e = lane; e < E; e += 32) {
             const uint32_t key = row[e];
             if (key > best) {
+                second = best;
+                at2 = at;
                 best = key;
                 at = e;
+            } else if (key > second) {
+                second = key;
+                at2 = e;
             }
         }
+    };
+    scan();
+    int my_idx = -1;
+    uint32_t my_key = 0u;
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) {
         const uint32_t kmax = __reduce_max_sync(0xffffffffu, best);
         const int win = (int)__reduce_min_sync(0xffffffffu, best == kmax ? at : 0xffffffffu);
-        if ((win & 31) == lane) row[win] = 0u;
         if (lane == j) {
             my_idx = win;
             my_key = kmax;
+        }
+        if ((win & 31) == lane) {
+            row[win] = 0u;
+            best = second;
+            at = at2;
+            second = 0u;
+            if (best == 0u) scan();
         }
     }
     float p = lane < k ? expf(order_key_float(my_key) - m) / s : 0.f;
