@@ -461,27 +461,17 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel) {
 // E4M3: the code's sign, exponent and mantissa moved to a bf16's fields are
 // the value times 2^-120 (subnormals included), so one bf16 product with
 // 2^(120 + se) finishes it; codes (2i, 2i + 1) of word j give pair 2j + i.
-// That factor is a bf16 while se <= 7 (weights below 2^16); larger scales take
-// the scalar decoder.
+// That factor is a bf16 while se <= 7 (weights below 2^16); a warp that meets a
+// larger scale multiplies twice.
 __device__ __forceinline__ void decode16_mx(uint32_t (&v)[8], const uint32_t (&c)[4], uint32_t scale, uint32_t by4) {
-    if (__builtin_expect(scale <= 134u, 1)) {
-        const uint32_t f = (scale + 120u) * 0x00800080u;
+    const uint32_t f = (scale + 120u) * 0x00800080u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t x = prmt(c[j], i ? 0xB3A2u : 0x9180u);  // a code and its sign, eight times, in each half
-                v[2 * j + i] = mul_bf16x2((x * by4) & 0x87F087F0u, f);
-            }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                v[2 * j + i] =
-                    quant::e4m3_scaled_bf16((uint8_t)(c[j] >> (16 * i)), (int)scale - 127) |
-                    (uint32_t)quant::e4m3_scaled_bf16((uint8_t)(c[j] >> (16 * i + 8)), (int)scale - 127) << 16;
-    }
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t x = prmt(c[j], i ? 0xB3A2u : 0x9180u);  // a code and its sign, eight times, in each half
+            v[2 * j + i] = mul_bf16x2((x * by4) & 0x87F087F0u, f);
+        }
 }
 // E2M1: likewise the value times 2^-126; the factor holds the E4M3 block scale
 // (not negative) times 2^118 -- the code's bits in a bf16's fields are s 2^-120,
@@ -550,23 +540,45 @@ __device__ __forceinline__ void few_step(float (&acc)[2][NT][4], uint32_t slot, 
         // lane (g, q) takes 16 codes of rows g and g + 8 of each tile (one block scale
         // each) and the same 16 token columns
         uint32_t v[2][2][8];
+        uint32_t c[2][2][FMT == 1 ? 4 : 2], sc[2][2];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int hi = 0; hi < 2; ++hi) {
                 int h;
                 const uint32_t rr = row(m, hi, h) + g;
-                const uint32_t wb = slot + (h * 2 + sub) * S::kChunkBytes, sc = slot + S::kWBytes + (h * 2 + sub) * S::kRun;
+                const uint32_t wb = slot + (h * 2 + sub) * S::kChunkBytes, sb = slot + S::kWBytes + (h * 2 + sub) * S::kRun;
                 if constexpr (FMT == 1) {
-                    uint32_t c[4];
-                    lds128(c, wb + rr * 128 + (((half * 4 + q) ^ (rr & 7)) << 4));
-                    decode16_mx(v[m][hi], c, lds8(sc + rr * 4 + half * 2 + (q >> 1)), sh.by4);
+                    lds128(c[m][hi], wb + rr * 128 + (((half * 4 + q) ^ (rr & 7)) << 4));
+                    sc[m][hi] = lds8(sb + rr * 4 + half * 2 + (q >> 1));
                 } else {
-                    uint32_t c[2];
-                    lds64(c, wb + rr * 64 + (((half * 2 + (q >> 1)) ^ ((rr >> 1) & 3)) << 4) + (q & 1) * 8);
-                    decode16_nv(v[m][hi], c, lds8(sc + rr * 8 + half * 4 + q), sh);
+                    lds64(c[m][hi], wb + rr * 64 + (((half * 2 + (q >> 1)) ^ ((rr >> 1) & 3)) << 4) + (q & 1) * 8);
+                    sc[m][hi] = lds8(sb + rr * 8 + half * 4 + q);
                 }
             }
+        if constexpr (FMT == 1) {
+            if (__any_sync(0xffffffffu, max(max(sc[0][0], sc[0][1]), max(sc[1][0], sc[1][1])) > 134u)) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int hi = 0; hi < 2; ++hi) {
+                        const uint32_t low = min(sc[m][hi], 134u), rest = (sc[m][hi] - low + 127u) * 0x00800080u;
+                        decode16_mx(v[m][hi], c[m][hi], low, sh.by4);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[m][hi][i] = mul_bf16x2(v[m][hi][i], rest);
+                    }
+            } else {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int hi = 0; hi < 2; ++hi) decode16_mx(v[m][hi], c[m][hi], sc[m][hi], sh.by4);
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) decode16_nv(v[m][hi], c[m][hi], sc[m][hi], sh);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -600,8 +612,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *xch = reinterpret_cast<float *>(ring + (size_t)kSlots * S::kSlotBytes);  // group 1's sums; projection sums
     FewRouting &r = *reinterpret_cast<FewRouting *>(xch + S::kXchFloats + S::kRowFloats);
-    uint64_t *fullw = reinterpret_cast<uint64_t *>((reinterpret_cast<uintptr_t>(&r + 1) + 7) & ~uintptr_t(7));
-    uint64_t *fullb = fullw + kSlots, *empty = fullb + kSlots, *routed = empty + kSlots;
+    uint64_t *full = reinterpret_cast<uint64_t *>((reinterpret_cast<uintptr_t>(&r + 1) + 7) & ~uintptr_t(7));
+    uint64_t *empty = full + kSlots, *routed = empty + kSlots;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(routed + 1);
     volatile int *last_flag = abort_flag + 1;
     const FewArgs &a = p.a;
@@ -609,8 +621,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kSlots; ++s) {
-            mbar_init(&fullw[s], 1);
-            mbar_init(&fullb[s], 1);
+            mbar_init(&full[s], 2);  // the two producers
             mbar_init(&empty[s], kFewConsumers / 32);
         }
         mbar_init(routed, 1);
@@ -630,6 +641,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 
     if (warp == kFewConsumers / 32) {
         // ================= weight producer =================
+        if (lane < 8) prefetch_tmap(&maps.gate + lane);  // all eight: a first use costs a microsecond otherwise
         if (lane == 0) {
             const uint64_t pol = policy_evict_first();
             uint32_t st = 0, ph = 0, issued = 0;
@@ -643,13 +655,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 }
                 uint8_t *dst = ring + (size_t)st * S::kSlotBytes;
                 const uint32_t run = S::kRun * (uint32_t)min(2, cols - kcol);
-                mbar_arrive_expect_tx(&fullw[st], S::kWBytes + 2 * run);
-                tma_load_3d_hint(m0, &fullw[st], dst, 0, y0, kcol, pol);
-                tma_load_3d_hint(m1, &fullw[st], dst + S::kWBytes / 2, 0, y1, kcol, pol);
+                mbar_arrive_expect_tx(&full[st], S::kWBytes + 2 * run);
+                tma_load_3d_hint(m0, &full[st], dst, 0, y0, kcol, pol);
+                tma_load_3d_hint(m1, &full[st], dst + S::kWBytes / 2, 0, y1, kcol, pol);
                 if constexpr (FMT != 0) {
-                    bulk_load(dst + S::kWBytes, f0 + ((size_t)(y0 >> 6) * cols + kcol) * S::kRun, run, &fullw[st]);
+                    bulk_load(dst + S::kWBytes, f0 + ((size_t)(y0 >> 6) * cols + kcol) * S::kRun, run, &full[st]);
                     bulk_load(dst + S::kWBytes + 2 * S::kRun, f1 + ((size_t)(y1 >> 6) * cols + kcol) * S::kRun, run,
-                              &fullw[st]);
+                              &full[st]);
                 }
                 ++issued;
                 if (++st == (uint32_t)kSlots) {
@@ -684,7 +696,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 }
             }
             for (uint32_t n = issued > (uint32_t)kSlots ? issued - kSlots : 0; n < issued; ++n)  // copies in flight
-                mbar_wait(&fullw[n % kSlots], (n / kSlots) & 1u, abort_flag, a.status, false);
+                mbar_wait(&full[n % kSlots], (n / kSlots) & 1u, abort_flag, a.status, false);
         }
     } else if (warp == kFewConsumers / 32 + 1) {
         // ================= token producer =================
@@ -711,8 +723,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                         const int u = (at - sS) / sI;
                         chunk = kS + u * kI + 2 * (at - sS - u * sI);
                     }
-                    mbar_arrive_expect_tx(&fullb[st], bytes);
-                    tma_load_3d_hint(map, &fullb[st], ring + (size_t)st * S::kSlotBytes + S::kTokOff, 0, 0,
+                    mbar_arrive_expect_tx(&full[st], bytes);
+                    tma_load_3d_hint(map, &full[st], ring + (size_t)st * S::kSlotBytes + S::kTokOff, 0, 0,
                                      chunk * S::kBoxes, policy_evict_normal());
                     ++issued;
                     if (++st == (uint32_t)kSlots) {
@@ -723,7 +735,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 }
             }
             for (uint32_t n = issued > (uint32_t)kSlots ? issued - kSlots : 0; n < issued; ++n)
-                mbar_wait(&fullb[n % kSlots], (n / kSlots) & 1u, abort_flag, a.status, false);
+                mbar_wait(&full[n % kSlots], (n / kSlots) & 1u, abort_flag, a.status, false);
         }
     } else if (warp >= kFewConsumers / 32 + 2) {
         // ================= routers =================
@@ -860,8 +872,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 for (int i = 0; i < n_steps; ++i) {
                     // the shared expert's channels come first: their sum takes the gate before the routed ones join
                     if (phase == 2 && at + i == sS && i > 0) scale_shared();
-                    if (!dead) dead = !mbar_wait_fast(&fullw[st], ph, abort_flag, a.status, true);
-                    if (!dead) dead = !mbar_wait_fast(&fullb[st], ph, abort_flag, a.status, true);
+                    if (!dead) dead = !mbar_wait_fast(&full[st], ph, abort_flag, a.status, true);
                     if (phase == 2 && !have_sg) {  // the token operand is past the grid barrier: so are the gates
                         have_sg = true;
 #pragma unroll
