@@ -46,6 +46,7 @@
 // operand): 16 significant bits, so that the result differs from fp32
 // arithmetic by its final rounding only.
 #include <atomic>
+#include <type_traits>
 
 #include "few.cuh"
 #include "front.cuh"
@@ -590,7 +591,7 @@ __device__ __forceinline__ void few_step(float (&acc)[2][NT][4], uint32_t slot, 
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     uint32_t b0 = b[2 * s], b1 = b[2 * s + 1];
-                    if constexpr (FMT == 2) {  // the columns in the codes' pair order
+                    if constexpr (FMT == 2 && !kDown) {  // the columns in the codes' pair order (h is stored in it)
                         const uint32_t lo = b[(s >> 1) * 4 + (s & 1)], hi = b[(s >> 1) * 4 + (s & 1) + 2];
                         b0 = __byte_perm(lo, hi, 0x5410);
                         b1 = __byte_perm(lo, hi, 0x7632);
@@ -850,58 +851,55 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             while (left > 0) {
                 const int n_steps = min(sh.per - at, left);
                 float acc[2][NT][4] = {};  // two tiles of 16 rows x 8 NT tokens
-                auto scale_shared = [&] {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            acc[m][n][0] *= sg[n][0];
-                            acc[m][n][1] *= sg[n][1];
-                            acc[m][n][2] *= sg[n][0];
-                            acc[m][n][3] *= sg[n][1];
-                        }
-                };
-                // steps until the odd last one of the unit's current K range
-                int in = at, range = phase < 2 ? sH : sS;
-                bool odd = (phase < 2 ? kH : kS) & 1;
-                if (phase == 2 && at >= sS) {
-                    in = (at - sS) % sI;
-                    range = sI;
-                    odd = kI & 1;
-                }
-                for (int i = 0; i < n_steps; ++i) {
-                    // the shared expert's channels come first: their sum takes the gate before the routed ones join
-                    if (phase == 2 && at + i == sS && i > 0) scale_shared();
+                // one step; the second chunk of an odd K range's last one is not there
+                auto take = [&](auto down, bool live) {
                     if (!dead) dead = !mbar_wait_fast(&full[st], ph, abort_flag, a.status, true);
-                    if (phase == 2 && !have_sg) {  // the token operand is past the grid barrier: so are the gates
-                        have_sg = true;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const int t = n * 8 + 2 * q + c;
-                                sg[n][c] = a.Is > 0 && t < a.T ? __ldcg(a.sgate + t) : 0.f;
-                            }
-                    }
-                    const bool live = sub == 0 || !(odd && in == range - 1);
-                    if (++in == range) {
-                        in = 0;
-                        range = sI;  // only the down projection goes on to another range
-                        odd = kI & 1;
-                    }
-                    if (live) {
-                        const uint32_t slot = smem_u32(ring + (size_t)st * S::kSlotBytes);
-                        if (phase == 2) few_step<FMT, NT, true>(acc, slot, rg, sub, half, lane, p.shifts);
-                        else few_step<FMT, NT, false>(acc, slot, rg, sub, half, lane, p.shifts);
-                    }
+                    if (live)
+                        few_step<FMT, NT, decltype(down)::value>(acc, smem_u32(ring + (size_t)st * S::kSlotBytes), rg, sub, half,
+                                                                 lane, p.shifts);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&empty[st]);
                     if (++st == (uint32_t)kSlots) {
                         st = 0;
                         ph ^= 1u;
                     }
+                };
+                if (phase < 2) {
+                    const int cut = sub & kH ? sH - 1 : sH;  // (sub is 0 or 1)
+                    for (int i = at; i < at + n_steps; ++i) take(std::false_type(), i != cut);
+                } else {
+                    int i = at;
+                    const int end = at + n_steps, cut = sub & kS ? sS - 1 : sS;
+                    for (; i < min(end, sS); ++i) take(std::true_type(), i != cut);
+                    if (i > at) {
+                        // the shared expert's channels come first: their sum takes the gate before the
+                        // routed ones join.  The token operand is past the grid barrier: so are the gates
+                        if (!have_sg)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    const int t = n * 8 + 2 * q + c;
+                                    sg[n][c] = t < a.T ? __ldcg(a.sgate + t) : 0.f;
+                                }
+                        have_sg = true;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                acc[m][n][0] *= sg[n][0];
+                                acc[m][n][1] *= sg[n][1];
+                                acc[m][n][2] *= sg[n][0];
+                                acc[m][n][3] *= sg[n][1];
+                            }
+                    }
+                    int in = (i - sS) % sI;
+                    const int last_in = sub & kI ? sI - 1 : sI;
+                    for (; i < end; ++i) {
+                        take(std::true_type(), in != last_in);
+                        if (++in == sI) in = 0;
+                    }
                 }
-                if (phase == 2 && at < sS && at + n_steps <= sS) scale_shared();  // the shared part alone
                 // the groups' sums
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -975,7 +973,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                     if (whole && phase < 2) {
                         // gate (rows 0..7) and up (8..15) of one channel are in one thread
                         const int per = a.I / 64, u = phase ? unit / per : 0, e = phase ? r.list[u] : 0;
-                        const int ch = (phase ? unit % per : unit) * 64 + wr * 8 + g;
+                        // NVFP4: in the order of the down projection's code pairs, 0 4 1 5 2 6 3 7
+                        const int at8 = FMT == 2 ? (g & 3) * 2 + (g >> 2) : g;
+                        const int ch = (phase ? unit % per : unit) * 64 + wr * 8 + at8;
                         const uint32_t tokens = phase ? r.mask[e] : (1u << a.T) - 1u;
                         uint16_t *dst = p.h + (phase ? a.Is + (size_t)u * a.I : 0) + ch;
                         float tg = 1.f, tu = 1.f, td = 1.f;

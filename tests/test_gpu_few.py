@@ -124,6 +124,7 @@ def test_block_scaled_odd_blocks(fmt):
         w[2] *= 2.0 ** -40
         w[3, 5] = 1.5
         w[4, ::3] = 0.0
+        w[5, 32:64] *= 2.0 ** 18
     check(cfg, inp, fmt)
 
 
