@@ -76,12 +76,9 @@ struct FewRouting {
     int nu;
 };
 
-// Arrive on a grid barrier (one thread, after a CTA barrier of the writers: its
-// fence is cumulative over what they wrote), and wait for all of the grid.
-__device__ __forceinline__ void grid_arrive(int32_t *ctr) {
-    __threadfence();
-    atomicAdd(ctr, 1);
-}
+// Arrive on a grid barrier (one thread, after a CTA barrier of the writers), and
+// wait for all of the grid.
+__device__ __forceinline__ void grid_arrive(int32_t *ctr) { add_release(ctr, 1); }
 __device__ __forceinline__ bool grid_wait(int32_t *ctr, int arrivals, volatile int *abort_flag, int32_t *status) {
     const unsigned long long t0 = globaltimer();
     while (ld_acquire(ctr) < arrivals) {
@@ -237,10 +234,7 @@ __device__ __forceinline__ void few_route_shared(const FewArgs &a, FewRouting &r
             }
             if (lane == 0) __stcg(picks + t, r.keff[t]);
             __syncwarp();
-            if (lane == 0) {
-                __threadfence();
-                atomicAdd(ctr, 1);
-            }
+            if (lane == 0) add_release(ctr, 1);
         }
     if (tid == 0) grid_wait(ctr, a.T, abort_flag, a.status);
     named_bar_sync(5, kFewRouters);
@@ -939,11 +933,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                             __stcg(slot(cta) + n * 256, make_float4(sum[n][0], sum[n][1], sum[n][2], sum[n][3]));
                         named_bar_sync(4, 256);
                         if (tid == 0) {
-                            __threadfence();
                             int32_t *ctr = p.sync + 16 + phase * kFewMaxSms + first;
-                            const bool is_last = atomicAdd(ctr, 1) == last - first;
+                            const bool is_last = (int)add_acq_rel(reinterpret_cast<uint32_t *>(ctr), 1u) == last - first;
                             if (is_last) *ctr = 0;
-                            __threadfence();
                             *last_flag = is_last;
                         }
                         named_bar_sync(4, 256);

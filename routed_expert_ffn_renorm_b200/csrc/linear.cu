@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 }
             }
             done();
+            if constexpr (kF32) named_bar_sync(1, kLinEpi);  // (done() has one otherwise)
             // Once all shares are in, the tile's 32-column blocks are added up in share
             // order by whichever warps of its sharers (of the same lane quarter) are there
             // to take one: the last to arrive, and those that wait for it at the end of
@@ -441,9 +442,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (lane == 0 && (half == 0 || blocks > 1)) {
                 uint32_t v = 0;
                 if (half == 0) {
-                    __threadfence();
-                    v = atomicAdd(word, 1u) + 1u;
-                    __threadfence();
+                    v = add_acq_rel(word, 1u) + 1u;  // releases all of the CTA's partial: a barrier lies before
                 } else {
                     v = (uint32_t)ld_acquire(reinterpret_cast<const int32_t *>(word));
                 }
