@@ -280,7 +280,7 @@ __device__ __forceinline__ void few_choose(const FewArgs &a, FewRouting &r, int 
         for (int u = tid; u < nu; u += nthr) {
             const int e = r.list[u];
             float s = 0.f;
-#pragma unroll 8
+#pragma unroll 4
             for (int i = 0; i < Tk; ++i) s += r.idx[i] == e ? r.w[i] : 0.f;
             r.agg[u] = s;
         }
@@ -289,7 +289,7 @@ __device__ __forceinline__ void few_choose(const FewArgs &a, FewRouting &r, int 
         for (int u = tid; u < nu; u += nthr) {
             int rank = 0;
             const float mine = r.agg[u];
-#pragma unroll 8
+#pragma unroll 4
             for (int o = 0; o < nu; ++o) {
                 const float other = r.agg[o];
                 rank += (other > mine) | ((other == mine) & (o < u));
@@ -297,29 +297,26 @@ __device__ __forceinline__ void few_choose(const FewArgs &a, FewRouting &r, int 
             if (rank >= a.budget) r.mask[r.list[u]] = 0;
         }
         sync();
-        for (int t = tid; t < a.T; t += nthr) {
-            int32_t *ti = r.idx + t * a.k;
-            float *tw = r.w + t * a.k;
+        for (int t = tid >> 5; t < a.T; t += nthr >> 5) {  // a warp per token: the kept picks move up
             const int valid = r.keff[t];
-            int c = 0;
-            for (int j = 0; j < valid; ++j)
-                if (r.mask[ti[j]]) {
-                    const int e = ti[j];
-                    const float w = tw[j];
-                    ti[c] = e;
-                    tw[c] = w;
-                    ++c;
-                }
-            for (int j = c; j < a.k; ++j) {
-                ti[j] = -1;
-                tw[j] = 0.f;
-            }
+            const int e = lane < valid ? r.idx[t * a.k + lane] : 0;
+            float w = lane < valid ? r.w[t * a.k + lane] : 0.f;
+            const unsigned kept = __ballot_sync(0xffffffffu, lane < valid && r.mask[e] != 0);
+            const int c = __popc(kept), at = __popc(kept & ((1u << lane) - 1u));
             if (a.norm_topk && c > 0 && c < valid) {
-                float s = 0.f;
-                for (int j = 0; j < c; ++j) s += tw[j];
-                for (int j = 0; j < c; ++j) tw[j] = tw[j] / s;
+                float sum = 0.f;  // in slot order
+                for (unsigned m = kept; m; m &= m - 1) sum += __shfl_sync(0xffffffffu, w, __ffs(m) - 1);
+                w = w / sum;
             }
-            r.keff[t] = c;
+            if (kept >> lane & 1u) {
+                r.idx[t * a.k + at] = e;
+                r.w[t * a.k + at] = w;
+            }
+            if (lane >= c && lane < a.k) {
+                r.idx[t * a.k + lane] = -1;
+                r.w[t * a.k + lane] = 0.f;
+            }
+            if (lane == 0) r.keff[t] = c;
         }
         list();
     }
