@@ -50,7 +50,7 @@ namespace {
 using namespace tc;
 
 constexpr int kLinEpi = 256;                   // epilogue threads
-constexpr int kLinThreads = 96 + kLinEpi;
+constexpr int kLinThreads = 96 + kLinEpi + 32;
 constexpr int kLinMaxSms = 160;                // no device has more SMs (workspace sizing)
 constexpr int kLinSliceA = 128 * 128;          // 128 rows of W x 64 columns
 constexpr int kLinRing = 216 * 1024;           // at most
@@ -58,12 +58,16 @@ constexpr int kLinAccStride = 256;             // TMEM columns between the two a
 constexpr int kLinSegment = 8;                 // K slices summed in TMEM for fp32 out
 constexpr int kLinBand = 8;                    // row tiles of a band
 constexpr int kLinMaxStages = 16;
+constexpr int kLinStagedSlices = 32;           // staged epilogue up to this many K slices
+constexpr int kLinBlockBytes = 32 * 128 * 2;   // staged epilogue: 32 tokens x 128 channels, 8 blocks a tile
 constexpr int kLinMaxSplit = 12;               // shares of a tile, and two for unaligned ends
 constexpr unsigned long long kLinLingerNs = 30000;  // wait for a tile's other shares to help adding them
 
 struct __align__(64) LinMaps {
     CUtensorMap w;  // [N, K], box 64 x 128
     CUtensorMap x;  // [T, K], box 64 x Nt (pair: Nt / 2)
+    CUtensorMap r, r16;  // residual [T, N], box 128 x 32 and 128 x 16 (staged epilogue)
+    CUtensorMap o, o16;  // out [T, N], the same
 };
 
 struct LinPlan {
@@ -73,6 +77,7 @@ struct LinPlan {
     int waves;          // whole waves of tiles
     int rest, sharers;  // tiles left, workers that share their K slices (== rest: a tile each)
     int stages;
+    int staged;         // whole tiles' residual and output pass through shared memory
 };
 
 // The tiles of worker w (a CTA or a pair): its tile of every wave, then its share of the rest.
@@ -145,9 +150,7 @@ __device__ __forceinline__ void lin_store32(const LinearArgs &a, int t0, int cou
             if (kFull || i < count) out[i * ld] = f32_to_bf16_bits(v[i]);
     }
 }
-template <bool kF32>
-__device__ __forceinline__ void lin_epilogue(const LinearArgs &a, int t0, int count, int n, float bias,
-                                             const uint32_t (&res)[32], float (&v)[32]) {
+__device__ __forceinline__ void lin_activate(const LinearArgs &a, float bias, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] += bias;
     if (a.act == MOE_ACT_RELU) {
@@ -160,6 +163,11 @@ __device__ __forceinline__ void lin_epilogue(const LinearArgs &a, int t0, int co
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_SILU>(v[i]);
     }
+}
+template <bool kF32>
+__device__ __forceinline__ void lin_epilogue(const LinearArgs &a, int t0, int count, int n, float bias,
+                                             const uint32_t (&res)[32], float (&v)[32]) {
+    lin_activate(a, bias, v);
     if (a.residual) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(res[i] << 16);
@@ -167,6 +175,12 @@ __device__ __forceinline__ void lin_epilogue(const LinearArgs &a, int t0, int co
     if (n >= a.N) return;
     if (count >= 32) lin_store32<kF32, true>(a, t0, 32, n, v);
     else lin_store32<kF32, false>(a, t0, count, n, v);
+}
+
+// Stores of the staged epilogue: bulk groups, one per block.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {  // all but the newest N groups have been read out of shared memory
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // kF32: fp32 out, the K axis summed in segments of kLinSegment slices.
@@ -177,7 +191,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     constexpr int kBlocks = 2;              // kF32: 32-column blocks of a token tile per epilogue half
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t full[kLinMaxStages], empty[kLinMaxStages], tfull[2], tempty[2], mma_done;
+    __shared__ uint64_t full[kLinMaxStages], empty[kLinMaxStages], tfull[2], tempty[2], mma_done, rfull[8], bfull[8];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag, go_flag;
     const LinearArgs &a = p.a;
@@ -187,6 +201,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int workers = kPair ? (int)gridDim.x >> 1 : (int)gridDim.x;
     const uint32_t brows = kPair ? (uint32_t)p.Nt >> 1 : (uint32_t)p.Nt;  // token rows this CTA loads
     const uint32_t slice = kLinSliceA + (brows * 128 + 1023) / 1024 * 1024;
+    uint8_t *staging = ring + (size_t)p.stages * kSlices * slice;  // the staged epilogue's 8 blocks
     pdl_launch_dependents();
 
     if (threadIdx.x == 0) {
@@ -199,6 +214,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             mbar_init(&tempty[i], kPair ? 2 : 1);
         }
         mbar_init(&mma_done, 1);
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&rfull[i], 1);
+            mbar_init(&bfull[i], 4);
+        }
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -327,6 +346,83 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             else umma_commit(&mma_done);
             mbar_wait(&mma_done, 0, &abort_flag, a.status, false);
         }
+    } else if (warp == kLinThreads / 32 - 1) {
+        // ================= copies of the staged epilogue =================
+        // Pairs, bf16 out: the residual of a whole tile arrives by TMA in 8 blocks of 32
+        // tokens x 128 channels, the epilogue turns each into the output in place, and it
+        // leaves by TMA in rows of 256 bytes.  As a block leaves, the next tile's residual
+        // (or just the room for it) is made ready.  The direct form's 64-byte accesses and
+        // their latency held 8192 x 16384 x 256 with a residual at 2.3 TB/s.
+        if (kPair && !kF32 && p.staged && lane == 0) {
+            LinWalk walk(p, worker, workers);
+            uint32_t bpar = 0;
+            struct Place {
+                int n0, t0, tile_end, end;  // first channel and token, the tile's end in tokens, and the rows'
+            };
+            auto place = [&](int tile) {
+                int r, j;
+                lin_tile(p, tile, r, j);
+                const int n0 = r * 256 + (int)rank * 128, tile_end = (j + 1) * p.Nt;
+                return Place{n0, j * p.Nt, tile_end, n0 < a.N ? min(tile_end, a.T) : 0};
+            };
+            // tokens of a block: 0, 16 or 32 (also 32 where the rows end: TMA stops there)
+            auto tokens = [&](const Place &at, int blk) {
+                const int t = at.t0 + 32 * blk;
+                return t >= at.end ? 0 : t + 16 < at.tile_end ? 32 : 16;
+            };
+            auto make_ready = [&](const Place &at, int blk) {
+                const int rows = tokens(at, blk);
+                if (rows == 0) return;
+                if (a.residual) {
+                    mbar_arrive_expect_tx(&rfull[blk], rows * 256);
+                    tma_load_2d(rows == 32 ? &maps.r : &maps.r16, &rfull[blk], staging + blk * kLinBlockBytes, at.n0,
+                                at.t0 + 32 * blk);
+                } else {
+                    mbar_arrive(&rfull[blk]);
+                }
+            };
+            bool more = walk.next(tile, k0, k1) && k1 - k0 == p.nk, ok = true;
+            Place now{}, next = more ? place(tile) : now;
+            for (int blk = 0; more && blk < 8; ++blk) make_ready(next, blk);
+            // the two blocks that left last and whether the next tile (or this one) wants them
+            int qa = -1, qb = -1;
+            bool qa_next = false, qb_next = false;
+            auto flush = [&](int q, bool to_next) {
+                if (q >= 0) make_ready(to_next ? next : now, q);
+            };
+            while (more && ok) {
+                now = next;
+                qa_next = qb_next = false;
+                more = walk.next(tile, k0, k1) && k1 - k0 == p.nk;
+                if (more) next = place(tile);
+                for (int blk = 0; blk < 8; ++blk) {
+                    if (blk == qa || blk == qb) {  // narrow tiles: wanted already
+                        bulk_wait_read<0>();
+                        flush(qa, qa_next);
+                        flush(qb, qb_next);
+                        qa = qb = -1;
+                    }
+                    const int rows = tokens(now, blk);
+                    if (rows == 0) {
+                        if (more) make_ready(next, blk);  // not used by this tile
+                        continue;
+                    }
+                    ok = mbar_wait_fast(&bfull[blk], (bpar >> blk) & 1u, &abort_flag, a.status, true);
+                    if (!ok) break;
+                    bpar ^= 1u << blk;
+                    tma_store_2d(rows == 32 ? &maps.o : &maps.o16, staging + blk * kLinBlockBytes, now.n0,
+                                 now.t0 + 32 * blk);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    bulk_wait_read<2>();
+                    flush(qa, qa_next);
+                    qa = qb;
+                    qa_next = qb_next;
+                    qb = more ? blk : -1;
+                    qb_next = true;
+                }
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
     } else {
         // ================= epilogue =================
         const int q = warp & 3, half = (warp - 3) >> 2, row = q * 32 + lane;
@@ -335,6 +431,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (kPair && rank != 0) mbar_arrive_cluster(mapa(smem_u32(&tempty[acc]), 0));
             else mbar_arrive(&tempty[acc]);
         };
+        constexpr bool kCanStage = kPair && !kF32;
+        uint32_t rpar = 0;  // parity of the half's four block barriers
         LinWalk walk(p, worker, workers);
         for (uint32_t it = 0; walk.next(tile, k0, k1);) {
             int r, j;
@@ -343,7 +441,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const int t0 = j * p.Nt, cols = min(p.Nt, a.T - t0);
             const bool whole = k1 - k0 == p.nk;
             uint32_t next[32];  // the coming block's residual, read ahead of its sums
-            if (!kF32 && whole && half * 32 < cols) lin_residual(a, t0 + half * 32, n, next);
+            const bool staged = kCanStage && p.staged && whole;
+            if (!kF32 && !staged && whole && half * 32 < cols) lin_residual(a, t0 + half * 32, n, next);
             // the sums: in TMEM, or (kF32) of all segments but the last in registers
             float sum[kF32 ? kBlocks : 1][32];
             uint32_t acc = 0, tbase = 0;
@@ -380,6 +479,31 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 }
             };
             const float bias = a.bias && n < a.N ? bf16_bits_to_f32(__ldg(a.bias + n)) : 0.f;
+            if constexpr (kCanStage) {
+                if (staged) {
+                    const int n0 = n - row, nb = n0 < a.N ? (cols - half * 32 + 63) / 64 : 0;  // this half's blocks
+                    for (int b = 0; b < nb; ++b) {
+                        const int c0 = half * 32 + 64 * b, blk = 2 * b + half;
+                        uint16_t *buf = reinterpret_cast<uint16_t *>(staging + blk * kLinBlockBytes) + row;
+                        float v[32];
+                        tmem_ld32(tbase + (uint32_t)c0, v);
+                        lin_activate(a, bias, v);
+                        mbar_wait_fast(&rfull[blk], (rpar >> b) & 1u, &abort_flag, a.status, true);
+                        rpar ^= 1u << b;
+                        if (a.residual) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] += bf16_bits_to_f32(buf[i * 128]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) buf[i * 128] = f32_to_bf16_bits(v[i]);
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bfull[blk]);
+                    }
+                    done();
+                    continue;
+                }
+            }
             if (whole) {
                 if constexpr (kF32) {
 #pragma unroll
@@ -539,10 +663,22 @@ cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
     if (p.waves == 0) workers = p.sharers;
     const int brows = kPair ? p.Nt / 2 : p.Nt;
     const int stage = kSlices * (kLinSliceA + (brows * 128 + 1023) / 1024 * 1024);
-    p.stages = std::min(kLinMaxStages, kLinRing / stage);
+    // Whole tiles of pairs with bf16 out go through shared memory where TMA can take
+    // their rows (a stride of whole 16 bytes) and K is short, so that the epilogue
+    // counts: 8192 x 16384 x 256 with a residual 228 us direct and 161 us staged, 2000 x
+    // 8192 x 1024 41 and 36; 1000 x 5120 x 5120 51 and 53 (a shorter ring).
+    p.staged = kPair && !kF32 && p.waves > 0 && a.N % 8 == 0 && p.nk <= kLinStagedSlices;
+    const int staging = p.staged ? 8 * kLinBlockBytes : 0;
+    p.stages = std::min(kLinMaxStages, (kLinRing - staging) / stage);
     LinMaps m;
     if (!encode_2d(&m.w, a.w, a.N, a.K, 128) || !encode_2d(&m.x, a.x, a.T, a.K, brows)) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + (size_t)p.stages * stage;
+    m.r = m.r16 = m.o = m.o16 = m.x;  // not read
+    if (p.staged && (!encode_rows(&m.o, a.out, a.T, a.N, 128, 32) || !encode_rows(&m.o16, a.out, a.T, a.N, 128, 16)))
+        return cudaErrorInvalidValue;
+    if (p.staged && a.residual &&
+        (!encode_rows(&m.r, a.residual, a.T, a.N, 128, 32) || !encode_rows(&m.r16, a.residual, a.T, a.N, 128, 16)))
+        return cudaErrorInvalidValue;
+    const size_t smem = 1024 + (size_t)p.stages * stage + staging;
     static std::atomic<int> attr_set[64];  // per device: opted in to the ring's shared memory
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;

@@ -68,6 +68,19 @@ def test_fp32_out_keeps_the_sums(T, N, K):
     assert float((out.double() - want).norm() / want.norm()) < 32 * 2.0 ** -24
 
 
+@pytest.mark.parametrize("T,N,K", [(280, 9608, 72), (300, 9480, 2048), (5000, 1032, 72), (70, 20008, 40),
+                                   (2049, 4104, 264), (4100, 1288, 2056)])
+@pytest.mark.parametrize("act,bias,residual", [("none", False, False), ("silu", True, True), ("none", False, True)],
+                         ids=["plain", "all", "res"])
+def test_many_tiles(T, N, K, act, bias, residual):
+    """Whole waves of tiles: ragged last tokens and channels, K at the border of the staged epilogue."""
+    out = check(T, N, K, act, bias, residual, seed=9)
+    if residual:  # in place
+        x, w, b, r = make(T, N, K, bias, residual, 9)
+        moe.moe_linear(x, w, r, workspace(T, N, K), bias=b, activation=act, residual=r)
+        assert torch.equal(r, out)
+
+
 def test_large_values_and_activation_tails():
     for act in ("gelu", "silu", "relu"):
         x, w, b, _ = make(20, 96, 64, True, False, 3)
