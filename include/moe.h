@@ -424,8 +424,9 @@ int moe_forward(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const f
  *   - aux->counts, offsets, perm and slot_pos must be NULL (nothing is
  *     dispatched).  aux->logits receives projected logits, as in moe_forward.
  *   - Uses the workspace of moe_workspace_bytes(cfg, T' >= T), zeroed once
- *     (moe_status_clear); a launch leaves its counters at zero.  One workspace
- *     serves one stream at a time.
+ *     (moe_status_clear); a launch leaves its counters at zero, except one that
+ *     set MOE_STATUS_TIMEOUT: clear the workspace before its next use.  One
+ *     workspace serves one stream at a time.
  *   - The kernel is a cooperative launch of one block per SM (its blocks wait
  *     for one another, each wait bounded: MOE_STATUS_TIMEOUT); it can be
  *     captured into a CUDA graph.  Where such a launch is impossible it
@@ -457,7 +458,8 @@ int moe_forward_few_nvfp4(const moe_config_t *cfg, int32_t T, const moe_bf16_t *
  *   - out may be `residual` itself (bf16), in place; it must not overlap
  *     anything else.
  *   - ws: moe_linear_workspace_bytes(T, N, K) bytes (0 for bad sizes), zeroed
- *     once by moe_status_clear; one workspace serves one stream at a time. */
+ *     once by moe_status_clear (and again after MOE_STATUS_TIMEOUT); one workspace
+ *     serves one stream at a time. */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_RELU 1
 #define MOE_ACT_GELU 2

@@ -18,12 +18,12 @@
 // workspace as fp32 partials, and the last CTA to arrive adds them in CTA order
 // (the same bits on every run).
 //
-// Measured (bf16): 256 experts, 8 tokens, 5.06 GB of weights in 750 us, 6.7 TB/s;
-// the drafter layer (16 x 1024 experts, shared 2048), 7 tokens, 369 MB in 71 us,
-// of which about 14 us are the fill, the wait for h between the gate/up and the
+// Measured (bf16): 256 experts, 8 tokens, 5.06 GB of weights in 760 us, 6.6 TB/s;
+// the drafter layer (16 x 1024 experts, shared 2048), 7 tokens, 369 MB in 69 us,
+// of which about 12 us are the fill, the wait for h between the gate/up and the
 // down projection, and the last row blocks' partials.  Block-scaled weights are
-// paced by their decoding (integer pipe 40% busy on average, 60% in the stream):
-// MXFP8 3.6 TB/s, NVFP4 1.6 TB/s.
+// paced by the consumers' instructions, half of them decoding (about 2 a cycle):
+// MXFP8 4.5 TB/s, NVFP4 1.9 TB/s.
 //
 // Roles: one producer warp streams the weights into a shared-memory ring by TMA,
 // two chunks of the K axis in a 3-D box (one thread's copies cost 75 ns each:
