@@ -20,9 +20,9 @@
 // 5120 in 218 us, 6.2 TB/s); from about 200 tokens on the tensor cores bind, and a
 // pair halves each CTA's share of the token operand (8191 x 7168 x 7168 in 627 us,
 // 1.34 PFLOP/s, in a burst; 750 us, 1.12 PFLOP/s, under the power cap, 80 us of it
-// the epilogue's).  Pairs against single
-// CTAs at 5120 x 17408, us: 38 and 37 at 16 tokens, 39 and 37 at 64, 45 and 46 at
-// 128, 60 and 71 at 224; hence pairs above 64 tokens.
+// the epilogue's).  Pairs against single CTAs at 5120 x 17408, us: 38 and 37 at 16
+// tokens, 39 and 37 at 64, 45 and 46 at 128, 60 and 71 at 224; hence pairs above 64
+// tokens.
 //
 // Tiles go to the grid in whole waves, in bands of 8 row tiles so that a wave's
 // operands stay in L2; the tiles that would make up a last, partial wave have
@@ -33,11 +33,10 @@
 //
 // Roles: warps 0 and 1 TMA producers of W and of the tokens (one lane each),
 // warp 2 TMEM allocation and MMA issue (one lane), warps 3..10 epilogue (two to
-// each TMEM lane quarter, on alternate 32-column blocks), warp 11 the copies of the
-// staged epilogue.  A lane holds one
-// output channel, so a warp's store of one token covers 32 consecutive
-// channels.  Every wait is bounded: past the limit the kernel sets
-// MOE_STATUS_TIMEOUT and every role stops.
+// each TMEM lane quarter, on alternate 32-column blocks), warp 11 the copies of
+// the staged epilogue.  A lane holds one output channel, so a warp's direct store
+// of one token covers 32 consecutive channels.  Every wait is bounded: past the
+// limit the kernel sets MOE_STATUS_TIMEOUT and every role stops.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
