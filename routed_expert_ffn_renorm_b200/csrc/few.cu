@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             const int tid = threadIdx.x - kFewConsumers - 64;
             if (a.project && tid == 0) grid_wait(p.sync, (int)gridDim.x, abort_flag, a.status);
             named_bar_sync(5, kFewRouters);
-            few_route_shared(a, r, a.project ? few_splits(a) : 1, p.lpart, 
+            few_route_shared(a, r, a.project ? few_splits(a) : 1, p.lpart,
                              reinterpret_cast<uint32_t *>(xch + S::kXchFloats), p.picks,
                              p.sync + 3, tid, abort_flag);
             few_choose(a, r, tid, kFewRouters, 5);
