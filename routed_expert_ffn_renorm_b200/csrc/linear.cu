@@ -188,7 +188,7 @@ template <bool kPair, bool kF32>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinPlan p) {
     constexpr int kSlices = kPair ? 1 : 2;  // K slices per stage: one barrier round trip for two small ones
-    constexpr int kBlocks = 2;              // kF32: 32-column blocks of a token tile per epilogue half
+    constexpr int kBlocks = kPair ? 3 : 1;  // kF32: 32-column blocks of a token tile per epilogue half
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[kLinMaxStages], empty[kLinMaxStages], tfull[2], tempty[2], mma_done, rfull[8], bfull[8];
@@ -629,10 +629,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // Single CTAs up to this many tokens, pairs above (figures at the top).
 constexpr int kLinSingleTokens = 64;
 
-// Token tile: the tokens in as few tiles of at most 256 (fp32 out: 128, the sums a
-// thread holds) as hold them, rounded up to 16.
+// Token tile: the tokens in as few tiles of at most 256 (fp32 out: 192, whose sums a
+// thread holds in 96 registers; 128 took 800 us for 8000 x 6000 x 6000, 192 takes 600)
+// as hold them, rounded up to 16.
 int lin_token_tile(int T, bool f32) {
-    const int most = f32 ? 128 : 256, tiles = (T - 1) / most + 1;
+    const int most = f32 ? 192 : 256, tiles = (T - 1) / most + 1;
     return ((T - 1) / tiles + 16) / 16 * 16;
 }
 
