@@ -177,6 +177,31 @@ __device__ __forceinline__ void lin_epilogue(const LinearArgs &a, int t0, int co
     else lin_store32<kF32, false>(a, t0, count, n, v);
 }
 
+// v += the partials of shares first .. last in order, 4 kVecs columns each, kShares
+// of them in flight (behind the last: the last's again, not added).
+template <int kShares, int kVecs, typename Part>
+__device__ __forceinline__ void lin_add(float (&v)[32], int first, int last, Part part) {
+    for (int w0 = first; w0 <= last; w0 += kShares) {
+        float4 o[kShares][kVecs];
+#pragma unroll
+        for (int w = 0; w < kShares; ++w) {
+            const float4 *src = part(min(w0 + w, last));
+#pragma unroll
+            for (int c = 0; c < kVecs; ++c) o[w][c] = __ldcg(src + c * 128);
+        }
+#pragma unroll
+        for (int w = 0; w < kShares; ++w)
+            if (w0 + w <= last)
+#pragma unroll
+                for (int c = 0; c < kVecs; ++c) {
+                    v[4 * c] += o[w][c].x;
+                    v[4 * c + 1] += o[w][c].y;
+                    v[4 * c + 2] += o[w][c].z;
+                    v[4 * c + 3] += o[w][c].w;
+                }
+    }
+}
+
 // Stores of the staged epilogue: bulk groups, one per block.
 template <int N>
 __device__ __forceinline__ void bulk_wait_read() {  // all but the newest N groups have been read out of shared memory
@@ -440,6 +465,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const int n = (kPair ? r * 256 + (int)rank * 128 : r * 128) + row;
             const int t0 = j * p.Nt, cols = min(p.Nt, a.T - t0);
             const bool whole = k1 - k0 == p.nk;
+            const float bias = a.bias && n < a.N ? bf16_bits_to_f32(__ldg(a.bias + n)) : 0.f;
             uint32_t next[32];  // the coming block's residual, read ahead of its sums
             const bool staged = kCanStage && p.staged && whole;
             if (!kF32 && !staged && whole && half * 32 < cols) lin_residual(a, t0 + half * 32, n, next);
@@ -478,7 +504,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     if (elected) release(acc);
                 }
             };
-            const float bias = a.bias && n < a.N ? bf16_bits_to_f32(__ldg(a.bias + n)) : 0.f;
             if constexpr (kCanStage) {
                 if (staged) {
                     const int n0 = n - row, nb = n0 < a.N ? (cols - half * 32 + 63) / 64 : 0;  // this half's blocks
@@ -590,18 +615,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) v[c] = 0.f;
                 if (c0 < cols) lin_residual(a, t0 + c0, n, next);
-#pragma unroll 2
-                for (int w = first; w <= last; ++w) {
-                    const float4 *src = part(w) + c0 / 4 * 128;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float4 o = __ldcg(src + c * 128);
-                        v[4 * c] += o.x;
-                        v[4 * c + 1] += o.y;
-                        v[4 * c + 2] += o.z;
-                        v[4 * c + 3] += o.w;
-                    }
-                }
+                if (!kPair && p.Nt <= 16) lin_add<4, 4>(v, first, last, [&](int w) { return part(w) + c0 / 4 * 128; });
+                else lin_add<kF32 && kPair ? 1 : 2, 8>(v, first, last, [&](int w) { return part(w) + c0 / 4 * 128; });
                 if (c0 < cols) lin_epilogue<kF32>(a, t0 + c0, cols - c0, n, bias, next, v);
                 if (blocks == 1) break;
             }
