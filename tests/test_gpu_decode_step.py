@@ -63,3 +63,53 @@ def test_step(L):
         torch.cuda.synchronize()
         assert torch.equal(tokens, first[0]) and torch.equal(logits, first[1])
     assert moe.status_read(ws) == 0 and moe.status_read(ws_l) == 0
+
+
+def test_operators_side_by_side_on_three_streams():
+    """The cooperative layer, shared linear tiles and verifications at the same
+    time, each stream with its own workspace: the same bits as alone."""
+    cfg = W.MoEConfig("side", T=9, H=1024, E=24, I=192, k=3, Is=256)
+    inp = W.make_inputs(cfg, device="cuda", seed=22, router=True, gate_std=0.5)
+    c, w = lib_config(cfg), weights_of(inp)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+
+    def n(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+    sizes = [(7, 3000, 2048), (200, 640, 4096), (300, 5000, 256)]
+    maps = [(n(T, K), n(N, K), n(T, N)) for T, N, K in sizes]
+    probs = torch.softmax(2 * torch.randn(6, 5, 3001, generator=g, device="cuda"), -1)
+    draft = torch.randint(0, 3001, (6, 4), generator=g, device="cuda").int()
+    u, us = torch.rand(6, 4, generator=g, device="cuda"), torch.rand(6, generator=g, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    ws = torch.zeros(moe.workspace_bytes(c, cfg.T), dtype=torch.uint8, device="cuda")
+    ws_l = torch.zeros(max(moe.linear_workspace_bytes(*s) for s in sizes), dtype=torch.uint8, device="cuda")
+    y, outs = torch.empty_like(inp.x), [torch.empty_like(r) for _, _, r in maps]
+    tokens, count = torch.empty(6, 5, dtype=torch.int32, device="cuda"), torch.empty(6, dtype=torch.int32, device="cuda")
+
+    def layer(stream):
+        moe.moe_forward_few(c, inp.x, None, w, y, ws, stream=stream)
+
+    def linear(stream):
+        for (x, m, r), out in zip(maps, outs):
+            moe.moe_linear(x, m, out, ws_l, activation="silu", residual=r, stream=stream)
+
+    def verify(stream):
+        moe.moe_verify(probs, draft, u, us, tokens, count, stream=stream)
+
+    calls = (layer, linear, verify)
+    torch.cuda.synchronize()
+    for call in calls:
+        call(streams[0])
+    torch.cuda.synchronize()
+    alone = [t.clone() for t in (y, *outs, tokens, count)]
+    for t in (y, *outs, tokens, count):
+        t.zero_()
+    torch.cuda.synchronize()
+    for i in range(40):
+        for call, stream in zip(calls, streams):
+            call(stream)
+    torch.cuda.synchronize()
+    assert moe.status_read(ws) == 0 and moe.status_read(ws_l) == 0
+    for got, want in zip((y, *outs, tokens, count), alone):
+        assert torch.equal(got, want)
