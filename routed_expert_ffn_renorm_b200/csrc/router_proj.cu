@@ -267,6 +267,7 @@ void rp_shape(int T, int E, int H, int sms, int *BN, int *S, int *kper) {
 }
 
 size_t rp_partial_bytes(int T, int E, int H) {
+    if (T == 0) return 0;  // no tile to split
     int BN, S, kper;
     rp_shape(T, E, H, kRpMaxSms, &BN, &S, &kper);  // the most splits any device takes
     return S > 1 ? (size_t)S * T * E * 4 : 0;
