@@ -19,7 +19,6 @@ import ctypes
 import os
 import threading
 from dataclasses import dataclass
-from functools import cached_property
 from typing import Optional
 
 __all__ = [
@@ -106,13 +105,9 @@ class MoEConfig:
     budget: int = 0
     topp: float = 0.0  # per-token top-p trim; 0 (or >= 1) = off
 
-    @cached_property
-    def _struct(self) -> _Config:
+    def _c(self) -> _Config:
         return _Config(self.hidden, self.n_routed_experts, self.moe_intermediate_size, self.num_experts_per_tok,
                        self.shared_intermediate_size, int(bool(self.norm_topk)), self.budget, float(self.topp))
-
-    def _c(self) -> _Config:
-        return self._struct
 
 
 @dataclass
