@@ -457,9 +457,9 @@ int moe_forward_few_nvfp4(const moe_config_t *cfg, int32_t T, const moe_bf16_t *
  *   - The result is the same bits on every run on the same GPU model.
  *   - out may be `residual` itself (bf16), in place; it must not overlap
  *     anything else.
- *   - ws: moe_linear_workspace_bytes(T, N, K) bytes (0 for bad sizes), zeroed
- *     once by moe_status_clear (and again after MOE_STATUS_TIMEOUT); one workspace
- *     serves one stream at a time. */
+ *   - ws: moe_linear_workspace_bytes(T', N, K) bytes, T' >= T (0 for bad sizes),
+ *     zeroed once by moe_status_clear (and again after MOE_STATUS_TIMEOUT); one
+ *     workspace serves one stream at a time. */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_RELU 1
 #define MOE_ACT_GELU 2

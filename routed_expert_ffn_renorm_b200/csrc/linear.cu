@@ -647,8 +647,9 @@ constexpr int kLinSingleTokens = 64;
 // Token tile: the tokens in as few tiles of at most 256 (fp32 out: 192, whose sums a
 // thread holds in 96 registers; 128 took 800 us for 8000 x 6000 x 6000, 192 takes 600)
 // as hold them, rounded up to 16.
+constexpr int kLinMaxTile = 256;
 int lin_token_tile(int T, bool f32) {
-    const int most = f32 ? 192 : 256, tiles = (T - 1) / most + 1;
+    const int most = f32 ? 192 : kLinMaxTile, tiles = (T - 1) / most + 1;
     return ((T - 1) / tiles + 16) / 16 * 16;
 }
 
@@ -726,8 +727,9 @@ cudaError_t launch_shape(const LinearArgs &a, int sms, cudaStream_t st) {
 size_t linear_scratch_bytes(int T, int N, int K) {
     (void)N;
     (void)K;
-    // two partials per CTA; a bf16 tile is never narrower than an fp32 one
-    return T == 0 ? 0 : (size_t)kLinMaxSms * 2 * 128 * ((lin_token_tile(T, false) + 31) / 32 * 32) * 4;
+    // two partials per CTA of the widest token tile that T or fewer tokens have (tiles
+    // are narrower again at 257 tokens than at 256), so that a workspace serves fewer too
+    return (size_t)kLinMaxSms * 2 * 128 * ((std::min(T, kLinMaxTile) + 31) / 32 * 32) * 4;
 }
 
 cudaError_t launch_linear(const LinearArgs &a, cudaStream_t st) {

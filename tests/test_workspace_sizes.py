@@ -16,3 +16,11 @@ def test_empty_batch_has_a_workspace(kw):
     c = _cfg(**kw)
     empty, one = (lib.moe_workspace_bytes(ctypes.byref(c), T) for T in (0, 1))
     assert 8192 <= empty <= one
+
+
+@pytest.mark.parametrize("N,K", [(1, 8), (4096, 4096), (131072, 5120), (300, 65536)])
+def test_a_linear_workspace_serves_fewer_tokens(N, K):
+    lib = moe.load_library()
+    sizes = [lib.moe_linear_workspace_bytes(T, N, K) for T in range(0, 2100)]
+    assert sizes == sorted(sizes) and sizes[0] == 8192
+    assert sizes[-1] <= lib.moe_linear_workspace_bytes(100000, N, K) < 43 << 20
