@@ -19,6 +19,8 @@ import ctypes
 import os
 import threading
 from dataclasses import dataclass
+from functools import lru_cache
+from math import prod
 from typing import Optional
 
 __all__ = [
@@ -587,6 +589,11 @@ def _expect_like(t, dtype, shape, device, name: str):
                          f"{t.device}")
 
 
+def _expect_device(t, device: int, name: str):
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected on cuda:{device}, got {t.device}")
+
+
 def _current_device(t, name: str):
     """The launch goes to the current device (its index is returned): its tensors have to live there."""
     if not t.is_cuda or t.get_device() != _torch()._C._cuda_getDevice():
@@ -594,30 +601,77 @@ def _current_device(t, name: str):
     return t.get_device()
 
 
+@lru_cache(maxsize=64)
+def _few_weight_spec(fn: str, H: int, E: int, I: int, Is: int, router: bool):
+    """(field, type, shape, or element count where the layout is packed) of the weights the call reads."""
+    torch = _torch()
+    bits = {"moe_forward_few": 16, "moe_forward_few_mxfp8": 8, "moe_forward_few_nvfp4": 4}[fn]
+    per = 2 if bits == 4 else 1  # weights per element
+    mats = [("w_gate", (E, I, H)), ("w_up", (E, I, H)), ("w_down", (E, H, I))]
+    if Is:
+        mats += [("ws_gate", (Is, H)), ("ws_up", (Is, H)), ("ws_down", (H, Is))]
+    spec = []
+    for name, shape in mats:
+        spec.append((name, torch.bfloat16 if bits == 16 else torch.uint8, shape[:-1] + (shape[-1] // per,)))
+        if bits < 16:
+            spec.append((name + "_scale", torch.uint8, prod(shape) // (4 * bits)))  # 32 or 16 weights a scale
+        if bits == 4 and len(shape) == 3:
+            spec.append((name + "_tscale", torch.float32, E))
+    if Is:
+        spec.append(("ws_gate_vec", torch.bfloat16, (H,)))
+        if bits == 4:
+            spec.append(("ws_tscale", torch.float32, 3))
+    if router:
+        spec.append(("w_router", torch.bfloat16, (E, H)))
+    return tuple(spec)
+
+
+def _check_few_weights(fn: str, cfg: MoEConfig, weights, device: int, router: bool):
+    """The kernel reads every weight in full: a tensor of another type, size or device would become an
+    out-of-bounds access."""
+    for name, dtype, shape in _few_weight_spec(fn, cfg.hidden, cfg.n_routed_experts, cfg.moe_intermediate_size,
+                                               cfg.shared_intermediate_size, router):
+        t = getattr(weights, name, None)
+        if t is None:
+            raise ValueError(f"{name} is missing from the weights")
+        if t.dtype is not dtype or t.get_device() != device or (
+                t.numel() if type(shape) is int else t.shape) != shape:
+            raise ValueError(f"{name}: expected {dtype} {shape} on cuda:{device}, got {t.dtype} {tuple(t.shape)} on "
+                             f"{t.device}")
+
+
+def _few_aux(cfg: MoEConfig, T: int, aux: dict, device: int) -> _Aux:
+    torch = _torch()
+    E, Tk = cfg.n_routed_experts, T * cfg.num_experts_per_tok
+    least = {"topk_idx": (torch.int32, Tk), "topk_w": (torch.float32, Tk), "sgate": (torch.float32, T),
+             "keff": (torch.int32, T), "expert_kept": (torch.uint8, E), "n_dropped": (torch.int32, 1),
+             "logits": (torch.float32, T * E)}
+    a = _Aux()
+    for name, t in aux.items():
+        if not hasattr(a, name):
+            raise ValueError(f"aux: no output {name!r}")
+        if name in least and t is not None:  # (the others the call refuses)
+            dtype, n = least[name]
+            if t.dtype is not dtype or t.numel() < n or t.get_device() != device:
+                raise ValueError(f"aux {name}: expected {n} elements of {dtype} on cuda:{device}, got {t.numel()} of "
+                                 f"{t.dtype} on {t.device}")
+        setattr(a, name, _ptr(t))
+    return a
+
+
 def _forward_few(fn: str, cfg: MoEConfig, x, logits, weights, out, ws, aux, stream):
     torch = _torch()
     dev = _current_device(x, "x")
-    T, H, E, I, Is = x.shape[0], cfg.hidden, cfg.n_routed_experts, cfg.moe_intermediate_size, \
-        cfg.shared_intermediate_size
+    T, H, E = x.shape[0], cfg.hidden, cfg.n_routed_experts
     _expect_like(x, torch.bfloat16, (T, H), dev, "x")
     _expect_like(out, torch.bfloat16, (T, H), dev, "out")
     if logits is not None:
         _expect_like(logits, torch.float32, (T, E), dev, "logits")
     elif weights.w_router is None:
         raise ValueError("logits is None and the weights have no w_router")
-    else:
-        _expect_like(weights.w_router, torch.bfloat16, (E, H), dev, "w_router")
-    per = {"moe_forward_few": 1, "moe_forward_few_mxfp8": 1, "moe_forward_few_nvfp4": 2}[fn]  # weights per element
-    if weights.w_gate.shape != (E, I, H // per) or weights.w_up.shape != (E, I, H // per) or \
-            weights.w_down.shape != (E, H, I // per):
-        raise ValueError("the expert weights' shapes differ from the configuration's")
-    if Is and (weights.ws_gate is None or weights.ws_gate.shape != (Is, H // per) or
-               weights.ws_up.shape != (Is, H // per) or weights.ws_down.shape != (H, Is // per) or
-               weights.ws_gate_vec.shape != (H,)):
-        raise ValueError("the shared expert's weights differ from the configuration's")
-    w, a = weights._c(), _Aux()
-    for name, t in (aux or {}).items():
-        setattr(a, name, _ptr(t))
+    _check_few_weights(fn, cfg, weights, dev, logits is None)
+    _expect_device(ws, dev, "ws")
+    w, a = weights._c(), _few_aux(cfg, T, aux, dev) if aux else _Aux()
     _check(fn, getattr(load_library(), fn)(
         ctypes.byref(cfg._c()), T, _ptr(x), _ptr(logits, True), ctypes.byref(w), _ptr(out), ctypes.byref(a),
         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
@@ -668,6 +722,7 @@ def moe_linear(x, w, out, ws, *, bias=None, activation: str = "none", residual=N
         _expect_like(residual, torch.bfloat16, (T, N), dev, "residual")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation: one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    _expect_device(ws, dev, "ws")
     _check("moe_linear", load_library().moe_linear(
         T, N, K, _ptr(x), _ptr(w), _ptr(bias, True), ACTIVATIONS[activation], _ptr(residual, True), _ptr(out),
         int(out.dtype == torch.float32), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
