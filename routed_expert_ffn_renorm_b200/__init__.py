@@ -596,7 +596,9 @@ def _expect_device(t, device: int, name: str):
 
 def _current_device(t, name: str):
     """The launch goes to the current device (its index is returned): its tensors have to live there."""
-    if not t.is_cuda or t.get_device() != _torch()._C._cuda_getDevice():
+    if not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}: tensors must live on a CUDA device")
+    if t.get_device() != _torch()._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_torch().cuda.current_device()}")
     return t.get_device()
 

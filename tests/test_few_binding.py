@@ -82,6 +82,18 @@ def test_outputs():
         moe._few_aux(CFG, T, {"topk_ids": torch.zeros(T, k, dtype=torch.int32)}, -1)
 
 
+def test_host_tensors_are_a_value_error():
+    """Also where there is no GPU to name as the current device."""
+    x, ws = torch.zeros(2, H, dtype=torch.bfloat16), torch.zeros(8192, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="x is on cpu"):
+        moe.moe_forward_few(CFG, x, None, weights("moe_forward_few"), x.clone(), ws)
+    with pytest.raises(ValueError, match="x is on cpu"):
+        moe.moe_linear(x, x.clone(), torch.zeros(2, 2), ws)
+    i = torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="target_probs is on cpu"):
+        moe.moe_verify(torch.zeros(1, 2, 4), i[:, :1], torch.zeros(1, 1), torch.zeros(1), i, i[0, :1])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("fn", CALLS)
 def test_calls(fn):
