@@ -86,6 +86,7 @@ int check_config(const moe_config_t *c, int32_t T) {
 
 bool aligned(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned_or_null(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool word_aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }  // single values; null too
 
 template <class T>
 T *at(void *ws, size_t off) {
@@ -138,7 +139,8 @@ int moe_budget(const moe_config_t *cfg, int32_t T, int32_t *topk_idx, float *top
     int rc = check_config(cfg, T);
     if (rc) return rc;
     if (T == 0) return MOE_OK;
-    if (!aligned(topk_idx) || !aligned(topk_w) || !aligned(keff) || !expert_kept || !n_dropped || !aligned(ws))
+    if (!aligned(topk_idx) || !aligned(topk_w) || !aligned(keff) || !expert_kept || !n_dropped ||
+        !word_aligned(n_dropped) || !aligned(ws))
         return MOE_ERR_INVALID_ARG;
     const WsLayout L = ws_layout(*cfg, T);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
@@ -543,7 +545,7 @@ int forward_impl(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const 
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     moe_aux_t a{};
     if (aux) a = *aux;
-    if (a.logits && !aligned(a.logits)) return MOE_ERR_INVALID_ARG;
+    if (!aligned_or_null(a.logits) || !word_aligned(a.n_dropped)) return MOE_ERR_INVALID_ARG;
     if (!logits) {  // router projection first
         float *lg = a.logits ? a.logits : at<float>(ws, L.logits);
         rc = moe_router_logits(cfg, T, x, w_router, lg, ws, ws_bytes, stream);
@@ -664,7 +666,7 @@ int few_impl(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const floa
     if (aux) a = *aux;
     if (a.counts || a.offsets || a.perm || a.slot_pos) return MOE_ERR_INVALID_ARG;  // nothing is dispatched
     if (!aligned_or_null(a.topk_idx) || !aligned_or_null(a.topk_w) || !aligned_or_null(a.sgate) ||
-        !aligned_or_null(a.keff) || !aligned_or_null(a.logits))
+        !aligned_or_null(a.keff) || !aligned_or_null(a.logits) || !word_aligned(a.n_dropped))
         return MOE_ERR_INVALID_ARG;
     const WsLayout L = ws_layout(*cfg, T);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
