@@ -150,24 +150,25 @@ __device__ __forceinline__ void lin_store32(const LinearArgs &a, int t0, int cou
             if (kFull || i < count) out[i * ld] = f32_to_bf16_bits(v[i]);
     }
 }
+template <bool kF32>
 __device__ __forceinline__ void lin_activate(const LinearArgs &a, float bias, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] += bias;
     if (a.act == MOE_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_RELU>(v[i]);
+        for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_RELU, kF32>(v[i]);
     } else if (a.act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_GELU>(v[i]);
+        for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_GELU, kF32>(v[i]);
     } else if (a.act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_SILU>(v[i]);
+        for (int i = 0; i < 32; ++i) v[i] = linear_act<MOE_ACT_SILU, kF32>(v[i]);
     }
 }
 template <bool kF32>
 __device__ __forceinline__ void lin_epilogue(const LinearArgs &a, int t0, int count, int n, float bias,
                                              const uint32_t (&res)[32], float (&v)[32]) {
-    lin_activate(a, bias, v);
+    lin_activate<kF32>(a, bias, v);
     if (a.residual) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(res[i] << 16);
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         uint16_t *buf = reinterpret_cast<uint16_t *>(staging + blk * kLinBlockBytes) + row;
                         float v[32];
                         tmem_ld32(tbase + (uint32_t)c0, v);
-                        lin_activate(a, bias, v);
+                        lin_activate<kF32>(a, bias, v);
                         mbar_wait_fast(&rfull[blk], (rpar >> b) & 1u, &abort_flag, a.status, true);
                         rpar ^= 1u << b;
                         if (a.residual) {
