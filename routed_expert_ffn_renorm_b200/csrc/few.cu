@@ -77,15 +77,16 @@ struct FewRouting {
 };
 
 // Arrive on a grid barrier (one thread, after a CTA barrier of the writers), and
-// wait for all of the grid.
+// wait for all of the grid.  `which` names the wait: 0 the logits, 1 h, 2 the picks.
 __device__ __forceinline__ void grid_arrive(int32_t *ctr) { add_release(ctr, 1); }
-__device__ __forceinline__ bool grid_wait(int32_t *ctr, int arrivals, volatile int *abort_flag, int32_t *status) {
+__device__ __forceinline__ bool grid_wait(const FewArgs &a, int which, int32_t *ctr, int arrivals,
+                                          volatile int *abort_flag) {
     const unsigned long long t0 = globaltimer();
-    while (ld_acquire(ctr) < arrivals) {
+    while (ld_acquire(ctr) < arrivals + (a.stall_wait == which)) {
         if (*abort_flag) return false;
-        if (globaltimer() - t0 > kWaitLimitNs) {
+        if (globaltimer() - t0 > a.wait_limit_ns) {
             *abort_flag = 1;
-            atomicOr(status, MOE_STATUS_TIMEOUT);
+            atomicOr(a.status, MOE_STATUS_TIMEOUT);
             return false;
         }
     }
@@ -241,13 +242,16 @@ __device__ __forceinline__ void few_route_shared(const FewArgs &a, FewRouting &r
             __syncwarp();
             if (lane == 0) add_release(ctr, 1);
         }
-    if (tid == 0) grid_wait(ctr, a.T, abort_flag, a.status);
+    if (tid == 0) grid_wait(a, 2, ctr, a.T, abort_flag);
     named_bar_sync(5, kFewRouters);
+    // after a wait that gave up the picks are whatever the scratch held: no index comes
+    // from them unchecked
     for (int s = tid; s < Tk; s += kFewRouters) {
-        r.idx[s] = __ldcg(picks + a.T + s);
+        const int e = __ldcg(picks + a.T + s);
+        r.idx[s] = (unsigned)e < (unsigned)a.E ? e : -1;
         r.w[s] = __int_as_float(__ldcg(picks + a.T + Tk + s));
     }
-    if (tid < a.T) r.keff[tid] = __ldcg(picks + tid);
+    if (tid < a.T) r.keff[tid] = min(max(__ldcg(picks + tid), 0), a.k);
 }
 
 // Apply the budget to the routed tokens and list the experts in use: threads
@@ -301,7 +305,7 @@ __device__ __forceinline__ void few_choose(const FewArgs &a, FewRouting &r, int 
             const int valid = r.keff[t];
             const int e = lane < valid ? r.idx[t * a.k + lane] : 0;
             float w = lane < valid ? r.w[t * a.k + lane] : 0.f;
-            const unsigned kept = __ballot_sync(0xffffffffu, lane < valid && r.mask[e] != 0);
+            const unsigned kept = __ballot_sync(0xffffffffu, lane < valid && e >= 0 && r.mask[e] != 0);
             const int c = __popc(kept), at = __popc(kept & ((1u << lane) - 1u));
             if (a.norm_topk && c > 0 && c < valid) {
                 float sum = 0.f;  // in slot order
@@ -607,12 +611,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     constexpr int kTp = S::kTp, kSlots = S::kSlots;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *xch = reinterpret_cast<float *>(ring + (size_t)kSlots * S::kSlotBytes);  // group 1's sums; projection sums
+    float *xch = reinterpret_cast<float *>(ring + (size_t)kSlots * S::kSlotBytes);  // the groups' sums; the projection's
     FewRouting &r = *reinterpret_cast<FewRouting *>(xch + S::kXchFloats + S::kRowFloats);
     uint64_t *full = reinterpret_cast<uint64_t *>((reinterpret_cast<uintptr_t>(&r + 1) + 7) & ~uintptr_t(7));
     uint64_t *empty = full + kSlots, *routed = empty + kSlots;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(routed + 1);
-    volatile int *last_flag = abort_flag + 1;
+    volatile int *last_flag = abort_flag + 1, *go_flag = last_flag + 1;
     const FewArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 if (phase == 1 && !mbar_wait(routed, 0, abort_flag, a.status, true)) break;
                 const Share sh = share(phase);
                 if (phase == 2) {
-                    if (!grid_wait(p.sync + 1, (int)gridDim.x, abort_flag, a.status)) break;
+                    if (!grid_wait(a, 1, p.sync + 1, (int)gridDim.x, abort_flag)) break;
                     fence_proxy_async_global();  // h was written by ordinary stores
                 }
                 const CUtensorMap *map = phase == 2 ? &maps.h : &maps.x;
@@ -742,7 +746,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         // token in every CTA: 16 warps, a token each, and one grid barrier less.
         if (a.Is > 0) {
             const int tid = threadIdx.x - kFewConsumers - 64;
-            if (a.project && tid == 0) grid_wait(p.sync, (int)gridDim.x, abort_flag, a.status);
+            if (a.project && tid == 0) grid_wait(a, 0, p.sync, (int)gridDim.x, abort_flag);
             named_bar_sync(5, kFewRouters);
             few_route_shared(a, r, a.project ? few_splits(a) : 1, p.lpart,
                              reinterpret_cast<uint32_t *>(xch + S::kXchFloats), p.picks,
@@ -821,7 +825,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         }
         if (a.Is == 0) {
             if (a.project) {
-                if (tid == 0) grid_wait(p.sync, (int)gridDim.x, abort_flag, a.status);
+                if (tid == 0) grid_wait(a, 0, p.sync, (int)gridDim.x, abort_flag);
                 consumers_sync();
             }
             // in the ring, which is empty till the routed experts are known
@@ -834,13 +838,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 
         const int grp = warp >> 2, rg = warp & 3, g = lane >> 2, q = lane & 3;
         const int sub = grp >> 1, half = grp & 1;  // this group's columns: a half of a chunk of the step
-        bool dead = false;  // a wait gave up: go through the motions to the end
+        bool dead = false;  // a wait for the ring gave up: go through the motions to the end
         uint32_t st = 0, ph = 0;
         float sg[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) sg[n][0] = sg[n][1] = 0.f;
         for (int phase = 0; phase < 3; ++phase) {
-            if (phase == 1 && a.Is > 0) dead |= !mbar_wait(routed, 0, abort_flag, a.status, true);
+            if (phase == 1) {
+                // the routing is read from here on, by every warp: one answer for all of them
+                // whether it is there (the named barriers below want all or none)
+                if (tid == 0) *go_flag = mbar_wait(routed, 0, abort_flag, a.status, true) && !*abort_flag;
+                consumers_sync();
+                if (!*go_flag) {
+                    if (tid == 0) grid_arrive(p.sync + 1);  // the other CTAs need not wait for this one
+                    break;
+                }
+            }
             const Share sh = share(phase);
             int unit = sh.lo / max(sh.per, 1), at = sh.lo - unit * sh.per, left = sh.hi - sh.lo;
             bool have_sg = false;
@@ -854,7 +867,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                         few_step<FMT, NT, decltype(down)::value>(acc, smem_u32(ring + (size_t)st * S::kSlotBytes), rg, sub, half,
                                                                  lane, p.shifts);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[st]);
+                    if (lane == 0 && !dead) mbar_arrive(&empty[st]);  // (a slot that never filled is not free)
                     if (++st == (uint32_t)kSlots) {
                         st = 0;
                         ph ^= 1u;

@@ -701,6 +701,7 @@ int few_impl(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const floa
     f.h = at<uint8_t>(ws, L.few);
     f.status = at<int32_t>(ws, L.status);
     f.sync = at<int32_t>(ws, kSyncOffset);
+    if (int rc = test_hooks(2, &f.wait_limit_ns, &f.stall_wait)) return rc;
     if constexpr (kDebugBounds)  // checked library: non-finite given logits are reported, not routed silently
         if (logits) {
             const int rc = cuda_rc(launch_check_logits((long long)T * f.E, logits, f.status, as_stream(stream)));

@@ -1,0 +1,73 @@
+"""The decode-step kernels when a wait runs out, without a fault.
+
+MOE_TEST_STALL_GROUP gives one of a kernel's waits a target that nothing reaches
+and MOE_TEST_WAIT_LIMIT_US shortens the limit.  The launch then has to end by
+itself, report MOE_STATUS_TIMEOUT and write nothing outside its buffers; the
+next call on the same workspace, cleared, gives the bits of a run before it.
+"""
+import pytest
+import torch
+
+import routed_expert_ffn_renorm_b200 as moe
+from routed_expert_ffn_renorm_b200 import workloads as W
+
+from parity_util import lib_config, weights_of
+from test_gpu_few import FORMS, cfg_
+
+pytestmark = pytest.mark.gpu
+
+
+def guarded(n, fill):
+    """n bytes of `fill` with 1 MB of 0x5A behind them."""
+    buf = torch.full((n + (1 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    buf[:n] = fill
+    return buf[:n], buf[n:]
+
+
+class Few:
+    """One call of the few-token layer whose scratch holds anything and whose buffers are guarded."""
+
+    def __init__(self, kw, fmt):
+        self.cfg = cfg_(H=512, E=24, I=256, k=4, **kw)
+        self.inp = W.make_inputs(self.cfg, device="cuda", seed=31, router=True, gate_std=0.5)
+        self.c, w = lib_config(self.cfg), weights_of(self.inp)
+        pack, self.call = FORMS[fmt]
+        self.w = pack(w) if pack else w
+        self.ws, self.ws_end = guarded(moe.workspace_bytes(self.c, self.cfg.T), 0xAB)
+        out, self.out_end = guarded(self.cfg.T * 512 * 2, 0)
+        self.out = out.view(torch.bfloat16).view(self.cfg.T, 512)
+
+    def run(self):
+        moe.status_clear(self.ws)
+        self.call(self.c, self.inp.x, None, self.w, self.out, self.ws)
+        status = moe.status_read(self.ws)
+        assert (self.ws_end == 0x5A).all() and (self.out_end == 0x5A).all()
+        return status, self.out.clone()
+
+
+FEW = [(dict(T=7, Is=128), 0), (dict(T=16, Is=256, budget=5), 2), (dict(T=1, Is=128), 0), (dict(T=9, budget=6), 0)]
+
+
+@pytest.mark.parametrize("kw,stall", FEW, ids=lambda v: str(v) if isinstance(v, int) else "_".join(
+    f"{a}{b}" for a, b in v.items()))
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+def test_few_routing_wait_runs_out(kw, stall, fmt, monkeypatch):
+    job = Few(kw, fmt)
+    status, want = job.run()
+    assert status == 0
+    monkeypatch.setenv("MOE_TEST_WAIT_LIMIT_US", "1000")
+    monkeypatch.setenv("MOE_TEST_STALL_GROUP", str(stall))
+    status, _ = job.run()
+    assert status == moe.MOE_STATUS_TIMEOUT
+    monkeypatch.undo()
+    status, got = job.run()
+    assert status == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("env", [{"MOE_TEST_WAIT_LIMIT_US": "0"}, {"MOE_TEST_STALL_GROUP": "3"}])
+def test_few_hooks_reject_bad_values(env, monkeypatch):
+    job = Few(dict(T=2), "bf16")
+    for k, v in env.items():
+        monkeypatch.setenv(k, v)
+    with pytest.raises(moe.MoEError):
+        job.run()
