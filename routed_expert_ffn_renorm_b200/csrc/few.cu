@@ -640,6 +640,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                                                               : Share(a.H / 128, sS + r.nu * sI);
     };
 
+    auto drain = [&](uint32_t issued) {  // a producer's copies in flight
+        unsigned long long until = 0;
+        for (uint32_t n = issued > (uint32_t)kSlots ? issued - kSlots : 0; n < issued; ++n)
+            until = mbar_drain(&full[n % kSlots], (n / kSlots) & 1u, abort_flag, a.status, until);
+    };
     if (warp == kFewConsumers / 32) {
         // ================= weight producer =================
         if (lane < 8) prefetch_tmap(&maps.gate + lane);  // all eight: a first use costs a microsecond otherwise
@@ -696,8 +701,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                     }
                 }
             }
-            for (uint32_t n = issued > (uint32_t)kSlots ? issued - kSlots : 0; n < issued; ++n)  // copies in flight
-                mbar_wait(&full[n % kSlots], (n / kSlots) & 1u, abort_flag, a.status, false);
+            drain(issued);
         }
     } else if (warp == kFewConsumers / 32 + 1) {
         // ================= token producer =================
@@ -735,8 +739,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                     if (++at == sh.per) at = 0;
                 }
             }
-            for (uint32_t n = issued > (uint32_t)kSlots ? issued - kSlots : 0; n < issued; ++n)
-                mbar_wait(&full[n % kSlots], (n / kSlots) & 1u, abort_flag, a.status, false);
+            drain(issued);
         }
     } else if (warp >= kFewConsumers / 32 + 2) {
         // ================= routers =================

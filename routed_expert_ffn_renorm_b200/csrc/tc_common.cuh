@@ -81,6 +81,26 @@ __device__ __forceinline__ bool mbar_wait_fast(uint64_t *bar, uint32_t parity, v
                                                int32_t *status, bool watch_abort) {
     return mbar_try_wait<kCl>(bar, parity) || mbar_wait<kCl>(bar, parity, abort_flag, status, watch_abort);
 }
+// Wait, at a role's end, for the copies it issued into a slot.  After an abort the
+// slot may never fill (another role's part of it is missing), while copies under
+// way land within microseconds: the waits that are left then end together, kDrainNs
+// after the first.  Returns that common end (0: no abort so far), for the next one.
+constexpr unsigned long long kDrainNs = 10000000ull;
+inline __device__ __noinline__ unsigned long long mbar_drain(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                                             int32_t *status, unsigned long long until) {
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+        if ((it & 15u) != 0) continue;
+        const unsigned long long now = globaltimer();
+        if (until == 0 && now - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            atomicOr(status, MOE_STATUS_TIMEOUT);
+        }
+        if (until == 0 && *abort_flag) until = now + kDrainNs;
+        if (until != 0 && now > until) break;
+    }
+    return until;
+}
 __device__ __forceinline__ void tma_load_2d(const CUtensorMap *map, uint64_t *bar, void *dst, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "

@@ -5,6 +5,8 @@ and MOE_TEST_WAIT_LIMIT_US shortens the limit.  The launch then has to end by
 itself, report MOE_STATUS_TIMEOUT and write nothing outside its buffers; the
 next call on the same workspace, cleared, gives the bits of a run before it.
 """
+import time
+
 import pytest
 import torch
 
@@ -59,6 +61,27 @@ def test_few_routing_wait_runs_out(kw, stall, fmt, monkeypatch):
     monkeypatch.setenv("MOE_TEST_STALL_GROUP", str(stall))
     status, _ = job.run()
     assert status == moe.MOE_STATUS_TIMEOUT
+    monkeypatch.undo()
+    status, got = job.run()
+    assert status == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kw", [dict(T=7, Is=128), dict(T=16), dict(T=1, Is=128)],
+                         ids=lambda kw: "_".join(f"{a}{b}" for a, b in kw.items()))
+@pytest.mark.parametrize("stall", [0, 1])
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_few_launch_ends_soon(kw, stall, fmt, monkeypatch):
+    """Every role stops once one has given up: no wait for a copy that nobody issued lasts its 4 s."""
+    job = Few(kw, fmt)
+    status, want = job.run()
+    assert status == 0
+    monkeypatch.setenv("MOE_TEST_WAIT_LIMIT_US", "1000")
+    monkeypatch.setenv("MOE_TEST_STALL_GROUP", str(stall))
+    t0 = time.perf_counter()
+    status, _ = job.run()
+    dt = time.perf_counter() - t0
+    assert status == moe.MOE_STATUS_TIMEOUT
+    assert dt < 2.0, f"the aborted launch took {dt:.2f} s"
     monkeypatch.undo()
     status, got = job.run()
     assert status == 0 and torch.equal(got, want)
