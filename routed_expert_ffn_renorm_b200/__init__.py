@@ -629,17 +629,24 @@ def _few_weight_spec(fn: str, H: int, E: int, I: int, Is: int, router: bool):
 
 
 def _check_few_weights(fn: str, cfg: MoEConfig, weights, device: int, router: bool):
-    """The kernel reads every weight in full: a tensor of another type, size or device would become an
-    out-of-bounds access."""
+    """The call's weight pointers.  The kernel reads every weight in full: a tensor of another type, size or
+    device would become an out-of-bounds access."""
+    ptrs = {}
     for name, dtype, shape in _few_weight_spec(fn, cfg.hidden, cfg.n_routed_experts, cfg.moe_intermediate_size,
                                                cfg.shared_intermediate_size, router):
         t = getattr(weights, name, None)
         if t is None:
             raise ValueError(f"{name} is missing from the weights")
         if t.dtype is not dtype or t.get_device() != device or (
-                t.numel() if type(shape) is int else t.shape) != shape:
-            raise ValueError(f"{name}: expected {dtype} {shape} on cuda:{device}, got {t.dtype} {tuple(t.shape)} on "
-                             f"{t.device}")
+                t.numel() if type(shape) is int else t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous {dtype} {shape} on cuda:{device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        ptrs[name] = t.data_ptr()
+    return _FEW_STRUCTS[fn](**ptrs)
+
+
+_FEW_STRUCTS = {"moe_forward_few": _Weights, "moe_forward_few_mxfp8": _WeightsMXFP8,
+                "moe_forward_few_nvfp4": _WeightsNVFP4}
 
 
 def _few_aux(cfg: MoEConfig, T: int, aux: dict, device: int) -> _Aux:
@@ -671,9 +678,9 @@ def _forward_few(fn: str, cfg: MoEConfig, x, logits, weights, out, ws, aux, stre
         _expect_like(logits, torch.float32, (T, E), dev, "logits")
     elif weights.w_router is None:
         raise ValueError("logits is None and the weights have no w_router")
-    _check_few_weights(fn, cfg, weights, dev, logits is None)
+    w = _check_few_weights(fn, cfg, weights, dev, logits is None)
     _expect_device(ws, dev, "ws")
-    w, a = weights._c(), _few_aux(cfg, T, aux, dev) if aux else _Aux()
+    a = _few_aux(cfg, T, aux, dev) if aux else _Aux()
     _check(fn, getattr(load_library(), fn)(
         ctypes.byref(cfg._c()), T, _ptr(x), _ptr(logits, True), ctypes.byref(w), _ptr(out), ctypes.byref(a),
         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
