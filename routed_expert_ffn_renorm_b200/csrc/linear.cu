@@ -36,7 +36,8 @@
 // each TMEM lane quarter, on alternate 32-column blocks), warp 11 the copies of
 // the staged epilogue.  A lane holds one output channel, so a warp's direct store
 // of one token covers 32 consecutive channels.  Every wait is bounded: past the
-// limit the kernel sets MOE_STATUS_TIMEOUT and every role stops.
+// limit the kernel sets MOE_STATUS_TIMEOUT, every role of the CTA or pair stops, and
+// what it has under way gets 10 ms to land.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -51,7 +52,6 @@ using namespace tc;
 
 constexpr int kLinEpi = 256;                   // epilogue threads
 constexpr int kLinThreads = 96 + kLinEpi + 32;
-constexpr int kLinMaxSms = 160;                // no device has more SMs (workspace sizing)
 constexpr int kLinSliceA = 128 * 128;          // 128 rows of W x 64 columns
 constexpr int kLinRing = 216 * 1024;           // at most
 constexpr int kLinAccStride = 256;             // TMEM columns between the two accumulators
@@ -209,6 +209,29 @@ __device__ __forceinline__ void bulk_wait_read() {  // all but the newest N grou
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// Bounded wait for a barrier (kCl: one that the other CTA of a pair arrives on).
+// False: the limit passed or a role has given up; in a pair both CTAs learn of it.
+template <bool kPair>
+__device__ __noinline__ bool lin_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status,
+                                           unsigned long long limit_ns) {
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t it = 1; !mbar_try_wait<kPair>(bar, parity); ++it) {
+        if ((it & 63u) != 0) continue;
+        if (*abort_flag) return false;
+        if (globaltimer() - t0 > limit_ns) {
+            *abort_flag = 1;
+            if (kPair) st_cluster_u32(mapa(smem_u32(const_cast<const int *>(abort_flag)), cluster_ctarank() ^ 1u), 1u);
+            atomicOr(status, MOE_STATUS_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+template <bool kPair, bool kCl = kPair>
+__device__ __forceinline__ bool lin_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, const LinPlan &p) {
+    return mbar_try_wait<kCl>(bar, parity) || lin_wait_slow<kPair>(bar, parity, abort_flag, p.a.status, p.a.wait_limit_ns);
+}
+
 // kF32: fp32 out, the K axis summed in segments of kLinSegment slices.
 template <bool kPair, bool kF32>
 __global__ void __launch_bounds__(kLinThreads, 1)
@@ -232,7 +255,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], 2);  // the two producers
+            mbar_init(&full[s], s == 0 && worker == a.stall_worker ? 3 : 2);  // the two producers
             mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -294,7 +317,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 for (int k = k0; k < k1; k += kSlices) {
                     const int n = min(kSlices, k1 - k);
                     if (issued >= (uint32_t)p.stages &&
-                        !mbar_wait_fast<kPair>(&empty[st], ph ^ 1u, &abort_flag, a.status, true)) {
+                        !lin_wait<kPair>(&empty[st], ph ^ 1u, &abort_flag, p)) {
                         ok = false;
                         break;
                     }
@@ -315,12 +338,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 }
             }
             // the copies still in flight (pair: released by the MMAs that read them)
-            for (uint32_t n = issued > (uint32_t)p.stages ? issued - p.stages : 0; n < issued; ++n) {
-                if constexpr (kPair)
-                    mbar_wait<true>(&empty[n % p.stages], (n / p.stages) & 1u, &abort_flag, a.status, false);
-                else
-                    mbar_wait(&full[n % p.stages], (n / p.stages) & 1u, &abort_flag, a.status, false);
-            }
+            unsigned long long until = 0;
+            for (uint32_t n = issued > (uint32_t)p.stages ? issued - p.stages : 0; n < issued; ++n)
+                until = mbar_drain(kPair ? &empty[n % p.stages] : &full[n % p.stages], (n / p.stages) & 1u, &abort_flag,
+                                   a.status, until);
         }
     } else if (warp == 2) {
         // ================= MMA issuer =================
@@ -333,13 +354,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             bool ok = true, more = walk.next(tile, k0, k1);
             for (uint32_t it = 0; ok && more; ++it) {
                 const uint32_t acc = it & 1u;
-                if (!mbar_wait_fast<kPair>(&tempty[acc], ((it >> 1) & 1u) ^ 1u, &abort_flag, a.status, true)) break;
+                if (!lin_wait<kPair>(&tempty[acc], ((it >> 1) & 1u) ^ 1u, &abort_flag, p)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * kLinAccStride;
                 const int end = kF32 ? min(k1, k0 + kLinSegment) : k1;
                 for (int k = k0; k < end; k += kSlices) {
                     const int n = min(kSlices, end - k);
-                    if (!mbar_wait_fast<kPair>(&full[st], ph, &abort_flag, a.status, true)) {
+                    if (!lin_wait<kPair>(&full[st], ph, &abort_flag, p)) {
                         ok = false;
                         break;
                     }
@@ -433,7 +454,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         if (more) make_ready(next, blk);  // not used by this tile
                         continue;
                     }
-                    ok = mbar_wait_fast(&bfull[blk], (bpar >> blk) & 1u, &abort_flag, a.status, true);
+                    ok = lin_wait<kPair, false>(&bfull[blk], (bpar >> blk) & 1u, &abort_flag, p);
                     if (!ok) break;
                     bpar ^= 1u << blk;
                     tma_store_2d(rows == 32 ? &maps.o : &maps.o16, staging + blk * kLinBlockBytes, now.n0,
@@ -448,6 +469,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 }
             }
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (!ok)  // residuals may be on their way
+                for (const unsigned long long t0 = globaltimer(); globaltimer() - t0 < kDrainNs;) {
+                }
         }
     } else {
         // ================= epilogue =================
@@ -478,7 +502,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             for (int k = k0; k < k1; k += kF32 ? kLinSegment : k1 - k0, ++it) {
                 acc = it & 1u;
                 tbase = tmem_base + acc * kLinAccStride + ((uint32_t)(q * 32) << 16);
-                if (elected) go_flag = mbar_wait<kPair>(&tfull[acc], (it >> 1) & 1u, &abort_flag, a.status, true);
+                if (elected) go_flag = lin_wait<kPair>(&tfull[acc], (it >> 1) & 1u, &abort_flag, p);
                 named_bar_sync(1, kLinEpi);
                 go = go_flag;
                 if (!go) break;
@@ -514,7 +538,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         float v[32];
                         tmem_ld32(tbase + (uint32_t)c0, v);
                         lin_activate<kF32>(a, bias, v);
-                        mbar_wait_fast(&rfull[blk], (rpar >> b) & 1u, &abort_flag, a.status, true);
+                        lin_wait<kPair, false>(&rfull[blk], (rpar >> b) & 1u, &abort_flag, p);
                         rpar ^= 1u << b;
                         if (a.residual) {
 #pragma unroll

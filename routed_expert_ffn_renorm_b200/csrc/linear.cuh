@@ -14,6 +14,8 @@ struct LinearArgs {
     int out_f32;
     int32_t *status, *sync;
     float *scratch;
+    unsigned long long wait_limit_ns;  // of the pipeline's waits, and a worker whose first
+    int stall_worker;                  // ring slot never fills (test_hooks)
 };
 
 // kExact: results that stay fp32.
@@ -33,8 +35,9 @@ __device__ __forceinline__ float linear_act(float v) {
     return v;
 }
 
+constexpr int kLinMaxSms = 160;  // no device has more SMs (workspace sizing)
 // Ints of the workspace head the kernel counts in (zero between launches).
-constexpr int kLinSyncInts = 4 * 160;
+constexpr int kLinSyncInts = 4 * kLinMaxSms;
 size_t linear_scratch_bytes(int T, int N, int K);
 cudaError_t launch_linear(const LinearArgs &a, cudaStream_t st);
 

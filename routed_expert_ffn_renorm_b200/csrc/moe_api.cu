@@ -789,8 +789,9 @@ int moe_linear(int32_t T, int32_t N, int32_t K, const moe_bf16_t *x, const moe_b
         !aligned(ws) || (out_f32 && static_cast<const void *>(residual) == out))
         return MOE_ERR_INVALID_ARG;
     if (ws_bytes < moe_linear_workspace_bytes(T, N, K)) return MOE_ERR_WORKSPACE;
-    const LinearArgs a{T,   N,       K, x, w, bias, residual, activation, out, out_f32, at<int32_t>(ws, 0),
-                       at<int32_t>(ws, kSyncOffset), at<float>(ws, kHeadBytes)};
+    LinearArgs a{T,   N,       K, x, w, bias, residual, activation, out, out_f32, at<int32_t>(ws, 0),
+                 at<int32_t>(ws, kSyncOffset), at<float>(ws, kHeadBytes)};
+    if (const int hooks = test_hooks(kLinMaxSms, &a.wait_limit_ns, &a.stall_worker)) return hooks;
     return cuda_rc(launch_linear(a, as_stream(stream)));
 }
 

@@ -145,7 +145,9 @@ cudaError_t launch_verify(int B, int L, int V, const float *p, const float *q, c
 //   grouped FFN: the wait of group `stall`'s down items for its gate/up items
 //     (most = E: the shared expert);
 //   few-token layer: the waits of the grid for the projected logits (0), for h (1)
-//     and for the tokens' picks (2).
+//     and for the tokens' picks (2);
+//   linear map: all of its pipeline's, and the first ring slot of worker `stall`
+//     (a CTA or a pair; none if the grid has fewer).
 int test_hooks(int most, unsigned long long *limit_ns, int *stall);
 
 // Grouped expert FFN (tcgen05).

@@ -15,6 +15,7 @@ from routed_expert_ffn_renorm_b200 import workloads as W
 
 from parity_util import lib_config, weights_of
 from test_gpu_few import FORMS, cfg_
+from test_gpu_linear import make
 
 pytestmark = pytest.mark.gpu
 
@@ -94,3 +95,52 @@ def test_few_hooks_reject_bad_values(env, monkeypatch):
         monkeypatch.setenv(k, v)
     with pytest.raises(moe.MoEError):
         job.run()
+
+
+LINEAR = [(7, 300, 1040), (7, 19200, 1040), (16, 4096, 1024), (64, 500, 8200), (70, 384, 5128), (224, 5120, 4096),
+          (280, 9608, 72), (300, 9480, 2048)]
+
+
+@pytest.mark.parametrize("T,N,K", LINEAR)
+@pytest.mark.parametrize("stall", [0, 3])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_wait_runs_out(T, N, K, stall, dtype, monkeypatch):
+    """A ring slot that never fills, in single CTAs and pairs, whole tiles (staged or not) and shared ones."""
+    x, w, b, r = make(T, N, K, True, True, 32)
+    size = 2 if dtype == torch.bfloat16 else 4
+    ws, ws_end = guarded(moe.linear_workspace_bytes(T, N, K), 0xAB)
+    out, out_end = guarded(T * N * size, 0)
+    out = out.view(dtype).view(T, N)
+
+    def run():
+        moe.status_clear(ws)
+        moe.moe_linear(x, w, out, ws, bias=b, activation="gelu", residual=r)
+        status = moe.status_read(ws)
+        assert (ws_end == 0x5A).all() and (out_end == 0x5A).all()
+        return status, out.clone()
+
+    status, want = run()
+    assert status == 0
+    monkeypatch.setenv("MOE_TEST_WAIT_LIMIT_US", "1000")
+    monkeypatch.setenv("MOE_TEST_STALL_GROUP", str(stall))
+    t0 = time.perf_counter()
+    status, _ = run()
+    dt = time.perf_counter() - t0
+    assert status == (moe.MOE_STATUS_TIMEOUT if stall < workers(T, N, K, dtype) else 0)
+    assert dt < 2.0, f"the aborted launch took {dt:.2f} s"
+    monkeypatch.undo()
+    status, got = run()
+    assert status == 0 and torch.equal(got, want)
+
+
+def workers(T, N, K, dtype):
+    """At least 4 CTAs or pairs, if the map has 4 row tiles or K slices to share."""
+    return 4 if (N + 255) // 256 >= 4 or K >= 2048 else 1
+
+
+def test_linear_hooks_reject_bad_values(monkeypatch):
+    x, w, _, _ = make(2, 16, 16, False, False)
+    ws = torch.zeros(moe.linear_workspace_bytes(2, 16, 16), dtype=torch.uint8, device="cuda")
+    monkeypatch.setenv("MOE_TEST_STALL_GROUP", "161")
+    with pytest.raises(moe.MoEError):
+        moe.moe_linear(x, w, torch.empty(2, 16, device="cuda"), ws)
