@@ -628,6 +628,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 ready = (v & 255u) == shares;
             }
             ready = __shfl_sync(0xffffffffu, ready, 0);
+            __syncwarp();  // lane 0's acquire lies before the other lanes' loads of the partials
             while (ready) {
                 int blk = 0;
                 if (blocks > 1) {
