@@ -33,7 +33,7 @@ struct FewArgs {
     void *h;        // scratch: row-block partials, then the gate/up activations
     int32_t *status, *sync;
     unsigned long long wait_limit_ns;  // of the grid's waits, and the one that stalls
-    int stall_wait;                    // (test_hooks)
+    int stall_wait;                    // (wait_hooks)
 };
 
 // Ints of the workspace head the kernel's counters take (zero between launches).

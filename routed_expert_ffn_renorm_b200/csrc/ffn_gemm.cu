@@ -1355,9 +1355,12 @@ int choose_tiles(const FfnArgs &a, int sms, int *bn, int *bns, int *pages) {
     return *pages >= min_pages(a.fmt) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
-}  // namespace
-
-int test_hooks(int most, unsigned long long *limit_ns, int *stall) {
+// Test hooks (failure-path tests only): MOE_TEST_WAIT_LIMIT_US in [1, 4e6]
+// shortens the fused launch's group-readiness wait, MOE_TEST_STALL_GROUP in
+// [0, E] (E: the shared expert) gives that group's down items a readiness
+// target its gate/up items never reach, so their wait runs out and the
+// launch ends with MOE_STATUS_TIMEOUT after the limit.  Unset: 4 s, none.
+int test_hooks(const FfnArgs &a, unsigned long long *limit_ns, int *stall) {
     *limit_ns = kWaitLimitNs;
     *stall = -1;
     if (const char *f = getenv("MOE_TEST_WAIT_LIMIT_US")) {
@@ -1369,11 +1372,13 @@ int test_hooks(int most, unsigned long long *limit_ns, int *stall) {
     if (const char *f = getenv("MOE_TEST_STALL_GROUP")) {
         char *end = nullptr;
         const long v = strtol(f, &end, 10);
-        if (*f == 0 || *end != 0 || v < 0 || v > most) return MOE_ERR_INVALID_ARG;
+        if (*f == 0 || *end != 0 || v < 0 || v > a.E) return MOE_ERR_INVALID_ARG;
         *stall = (int)v;
     }
     return MOE_OK;
 }
+
+}  // namespace
 
 // CTA pairs (cta_group::2) for a single-phase launch whose groups fill wide
 // token tiles: the mean group has at least 128 tokens (the regime where a
@@ -1422,7 +1427,7 @@ int ffn_launch(const FfnArgs &a, int phases, cudaStream_t st) {
     FfnParams p{};
     if (int rc = choose_tiles(a, di.sms, &p.BN, &p.BNs, &p.pages)) return rc;
     if (a.fmt && 2 * p.BN > kConvCol0) return MOE_ERR_UNSUPPORTED;  // accumulators end where the A buffers start
-    if (int rc = test_hooks(a.E, &p.wait_limit_ns, &p.stall_group)) return rc;
+    if (int rc = test_hooks(a, &p.wait_limit_ns, &p.stall_group)) return rc;
     bool pair = false;
     if (int rc = choose_pair(a, phases, di.sms, &pair)) return rc;
     const int BN = p.BN;

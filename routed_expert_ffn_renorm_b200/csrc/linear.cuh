@@ -15,7 +15,7 @@ struct LinearArgs {
     int32_t *status, *sync;
     float *scratch;
     unsigned long long wait_limit_ns;  // of the pipeline's waits, and a worker whose first
-    int stall_worker;                  // ring slot never fills (test_hooks)
+    int stall_worker;                  // ring slot never fills (wait_hooks)
 };
 
 // kExact: results that stay fp32.

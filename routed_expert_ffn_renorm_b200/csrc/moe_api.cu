@@ -3,12 +3,14 @@
 // moe_status_read, which waits for its own copy); every launch goes on the
 // caller's stream.
 #include <algorithm>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 
 #include "few.cuh"
 #include "linear.cuh"
 #include "moe_internal.cuh"
+#include "tc_common.cuh"
 
 using namespace moe;
 
@@ -645,6 +647,26 @@ int moe_forward_nvfp4(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, c
 
 }  // extern "C"
 
+namespace moe {
+
+int wait_hooks(int most, unsigned long long *limit_ns, int *stall) {
+    auto number = [](const char *name, long long lo, long long hi, long long *out) {  // unset: *out stays
+        const char *f = getenv(name);
+        if (!f) return true;
+        char *end = nullptr;
+        *out = strtoll(f, &end, 10);
+        return *f != 0 && *end == 0 && *out >= lo && *out <= hi;
+    };
+    long long us = (long long)(tc::kWaitLimitNs / 1000), group = -1;
+    if (!number("MOE_TEST_WAIT_LIMIT_US", 1, 4000000, &us) || !number("MOE_TEST_STALL_GROUP", 0, most, &group))
+        return MOE_ERR_INVALID_ARG;
+    *limit_ns = (unsigned long long)us * 1000ull;
+    *stall = (int)group;
+    return MOE_OK;
+}
+
+}  // namespace moe
+
 namespace {
 
 // The few-token layer around its weights: `m` holds the matrices in the order
@@ -701,7 +723,7 @@ int few_impl(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const floa
     f.h = at<uint8_t>(ws, L.few);
     f.status = at<int32_t>(ws, L.status);
     f.sync = at<int32_t>(ws, kSyncOffset);
-    if (int rc = test_hooks(2, &f.wait_limit_ns, &f.stall_wait)) return rc;
+    if (int rc = wait_hooks(2, &f.wait_limit_ns, &f.stall_wait)) return rc;
     if constexpr (kDebugBounds)  // checked library: non-finite given logits are reported, not routed silently
         if (logits) {
             const int rc = cuda_rc(launch_check_logits((long long)T * f.E, logits, f.status, as_stream(stream)));
@@ -791,7 +813,7 @@ int moe_linear(int32_t T, int32_t N, int32_t K, const moe_bf16_t *x, const moe_b
     if (ws_bytes < moe_linear_workspace_bytes(T, N, K)) return MOE_ERR_WORKSPACE;
     LinearArgs a{T,   N,       K, x, w, bias, residual, activation, out, out_f32, at<int32_t>(ws, 0),
                  at<int32_t>(ws, kSyncOffset), at<float>(ws, kHeadBytes)};
-    if (const int hooks = test_hooks(kLinMaxSms, &a.wait_limit_ns, &a.stall_worker)) return hooks;
+    if (const int hooks = wait_hooks(kLinMaxSms, &a.wait_limit_ns, &a.stall_worker)) return hooks;
     return cuda_rc(launch_linear(a, as_stream(stream)));
 }
 

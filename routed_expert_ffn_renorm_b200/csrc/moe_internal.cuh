@@ -138,17 +138,16 @@ cudaError_t launch_verify(int B, int L, int V, const float *p, const float *q, c
                           const int32_t *len, const float *u, const float *us, int32_t *tokens, int32_t *n_accepted,
                           cudaStream_t st);
 
-// Test hooks (failure-path tests only), by which a wait runs out on purpose and the
-// launch ends with MOE_STATUS_TIMEOUT: MOE_TEST_WAIT_LIMIT_US in [1, 4e6] shortens
-// the limit of the waits named below, MOE_TEST_STALL_GROUP in [0, most] gives one of
-// them a target that nothing reaches.  Unset: 4 s, none (-1).
-//   grouped FFN: the wait of group `stall`'s down items for its gate/up items
-//     (most = E: the shared expert);
+// Test hooks of the decode-step kernels (failure-path tests only; the grouped FFN has
+// its own of the same names), by which a wait runs out on purpose and the launch ends
+// with MOE_STATUS_TIMEOUT: MOE_TEST_WAIT_LIMIT_US in [1, 4e6] shortens the limit of
+// the waits named below, MOE_TEST_STALL_GROUP in [0, most] gives one of them a target
+// that nothing reaches.  Unset: 4 s, none (-1).
 //   few-token layer: the waits of the grid for the projected logits (0), for h (1)
 //     and for the tokens' picks (2);
 //   linear map: all of its pipeline's, and the first ring slot of worker `stall`
 //     (a CTA or a pair; none if the grid has fewer).
-int test_hooks(int most, unsigned long long *limit_ns, int *stall);
+int wait_hooks(int most, unsigned long long *limit_ns, int *stall);
 
 // Grouped expert FFN (tcgen05).
 struct FfnArgs {
