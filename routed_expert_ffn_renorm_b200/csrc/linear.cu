@@ -14,15 +14,15 @@
 // The tensor cores truncate at every addition to an accumulator, 4 per slice: at
 // K = 5120 an fp32 result was 5.5e-6 off, 30 times an fp32 sum's error.  fp32 out
 // therefore sums segments of 512 columns in TMEM and the segments in registers,
-// rounded to nearest (5e-7); for bf16 out the rounding hides the rest.
+// rounded to nearest (4.8e-7; segments of 256 columns 2.4e-7, and 74 us would be 86 at
+// 1000 x 5120 x 5120); for bf16 out the rounding hides the rest.
 //
 // Bound: few tokens stream W from HBM (one CTA per SM, single tiles: 7 x 131072 x
 // 5120 in 218 us, 6.2 TB/s); from about 200 tokens on the tensor cores bind, and a
-// pair halves each CTA's share of the token operand (8191 x 7168 x 7168 in 627 us,
-// 1.34 PFLOP/s, in a burst; 750 us, 1.12 PFLOP/s, under the power cap, 80 us of it
-// the epilogue's).  Pairs against single CTAs at 5120 x 17408, us: 38 and 37 at 16
-// tokens, 39 and 37 at 64, 45 and 46 at 128, 60 and 71 at 224; hence pairs above 64
-// tokens.
+// pair halves each CTA's share of the token operand (8191 x 7168 x 7168 in 740 to 755
+// us, 1.12 PFLOP/s, under the power cap, 80 us of it the epilogue's).  Pairs against
+// single CTAs at 5120 x 17408, us: 38 and 37 at 16 tokens, 39 and 37 at 64, 45 and 46
+// at 128, 60 and 71 at 224; hence pairs above 64 tokens.
 //
 // Tiles go to the grid in whole waves, in bands of 8 row tiles so that a wave's
 // operands stay in L2; the tiles that would make up a last, partial wave have
@@ -671,8 +671,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 constexpr int kLinSingleTokens = 64;
 
 // Token tile: the tokens in as few tiles of at most 256 (fp32 out: 192, whose sums a
-// thread holds in 96 registers; 128 took 800 us for 8000 x 6000 x 6000, 192 takes 600)
-// as hold them, rounded up to 16.
+// thread holds in 96 registers; 128 took 800 us for 8000 x 6000 x 6000, 192 takes 630 to
+// 675) as hold them, rounded up to 16.
 constexpr int kLinMaxTile = 256;
 int lin_token_tile(int T, bool f32) {
     const int most = f32 ? 192 : kLinMaxTile, tiles = (T - 1) / most + 1;
