@@ -431,9 +431,10 @@ int moe_forward(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const f
  *     for one another, each wait bounded: MOE_STATUS_TIMEOUT); it can be
  *     captured into a CUDA graph.  Where such a launch is impossible it
  *     returns MOE_ERR_CUDA.
- *   - An infinity or NaN in a token reaches that token alone.  One in an expert's
- *     weights reaches every token of the batch, not only those routed to it (the
- *     down projection multiplies them by zero): weights have to be finite.
+ *   - With finite logits, an infinity or NaN in a token reaches that token alone.
+ *     One in an expert's weights reaches every token of the batch, not only those
+ *     routed to it (the down projection multiplies them by zero): weights have to be
+ *     finite.
  *   - out must not overlap an input. */
 #define MOE_FEW_MAX_TOKENS 16
 int moe_forward_few(const moe_config_t *cfg, int32_t T, const moe_bf16_t *x, const float *logits,
@@ -458,8 +459,8 @@ int moe_forward_few_nvfp4(const moe_config_t *cfg, int32_t T, const moe_bf16_t *
  *   - The tensor cores truncate their sums; fp32 out therefore leaves them every
  *     512 columns: 4.2 to 4.8e-7 relative in the norm, where a library's fp32 product
  *     has 1 to 2e-7 for a few tokens and 6 to 8e-7 for more.
- *   - SiLU: fp32 out within 3 ulps of the sum's value; before a rounding to bf16 by
- *     the approximate exponential (2 + 1.2 |v| ulps of fp32).
+ *   - SiLU of a sum v: fp32 out within 3 ulps; before a rounding to bf16 by the
+ *     approximate exponential (2 + 1.2 |v| ulps of fp32, under the rounding's 32768).
  *   - The result is the same bits on every run on the same GPU model.
  *   - out may be `residual` itself (bf16), in place; it must not overlap
  *     anything else.

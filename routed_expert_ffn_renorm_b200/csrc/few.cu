@@ -21,9 +21,9 @@
 // Measured in a graph of calls (bf16): 256 experts, 8 tokens, 5.06 GB of weights in
 // 766 us, 6.6 TB/s; the drafter layer (16 x 1024 experts, shared 2048), 7 tokens,
 // 369 MB in 69 to 72 us, of which about 12 us are the fill, the wait for h between
-// the gate/up and the down projection, and the last row blocks' partials.  Block-scaled weights are
-// paced by the consumers' instructions, half of them decoding (about 2 a cycle):
-// MXFP8 4.5 TB/s, NVFP4 1.9 TB/s.
+// the gate/up and the down projection, and the last row blocks' partials.
+// Block-scaled weights are paced by the consumers' instructions, half of them
+// decoding (about 2 a cycle): MXFP8 4.5 TB/s, NVFP4 1.9 TB/s.
 //
 // Roles: one producer warp streams the weights into a shared-memory ring by TMA,
 // two chunks of the K axis in a 3-D box (one thread's copies cost 75 ns each:
